@@ -1,4 +1,5 @@
-"""Python binding of libk3mx.so, the C ABI declared in include/k3mx.h.
+"""Python binding of libk3mx.so, the C ABI declared in include/k3mx.h and
+include/k3mx_mx.h.
 
 Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  The functions carry the C names; tensors are passed as their
@@ -23,6 +24,7 @@ K3MX_LATENT = 3584
 K3MX_INTER = 3072
 K3MX_EXPERT_BYTES = 17547264
 K3MX_F32, K3MX_BF16 = 0, 1
+K3MX_MXFP4, K3MX_MXFP8 = 0, 1
 K3MX_PATH_AUTO, K3MX_PATH_DECODE, K3MX_PATH_PREFILL, K3MX_PATH_PREFILL_MX = 0, 1, 2, 3
 K3MX_PREFILL_MIN_TOKENS = 256
 K3MX_MAX_TOKENS = 65536
@@ -66,7 +68,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build(); "
                                "this package has no CPU fallback")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        vp, i, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
         sig = {
             "k3mx_gemv": ([vp, vp, vp, vp, i, i, vp], i),
             "k3mx_expert_ffn_workspace_size": ([], sz),
@@ -89,6 +91,11 @@ def lib():
             "k3mx_status_str": ([i], ctypes.c_char_p),
             "k3mx_last_cuda_error": ([], ctypes.c_char_p),
             "k3mx_abi_version": ([], i),
+            "k3mx_mx_quantize": ([vp, vp, vp, i, i, i, i64, i, vp], i),
+            "k3mx_mx_dequantize": ([vp, i, vp, vp, i, i, i, vp], i),
+            "k3mx_rmsnorm_mx": ([vp, vp, vp, vp, vp, i64, vp, i, vp, ctypes.c_float, i, i, vp], i),
+            "k3mx_mx_linear": ([vp, i, vp, vp, vp, vp, i, i, i, vp], i),
+            "k3mx_mx_grouped": ([vp, i, vp, vp, vp, vp, vp, i, i, i, i, vp], i),
             "k3mx_trace_enable": ([i], i),
             "k3mx_trace_read": ([ctypes.POINTER(TraceEntry), i], i),
         }
@@ -422,6 +429,153 @@ def k3mx_moe_routed_host(y_host, x_host, experts, logits_host, bias_host, worksp
         _ptr(bias_host), path, _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
     return y_host
+
+
+# ------------------------------------------------ microscaled operators --
+
+_MX_DTYPES = {torch.float32: K3MX_F32, torch.bfloat16: K3MX_BF16}
+
+
+def _mx_dtype(t, name):
+    dt = _MX_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dt is None:
+        raise TypeError(f"{name}: float32 or bfloat16 tensor expected")
+    return dt
+
+
+def _mx_shape(t, shape, name):
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
+        got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
+        raise TypeError(f"{name}: shape {list(shape)} expected, got {got}")
+
+
+def _mx_matrix(codes, scales, rows, cols, fmt, names=("codes", "scales")):
+    """Shapes of a microscaled matrix of rows x cols (the sizes a call passes on)."""
+    if fmt not in (K3MX_MXFP4, K3MX_MXFP8):
+        raise ValueError(f"fmt: K3MX_MXFP4 or K3MX_MXFP8 expected, got {fmt!r}")
+    if rows < 1 or cols < 32 or cols % 32:
+        raise TypeError(f"{names[0]}: at least one row and columns in blocks of 32 expected, got {rows} x {cols}")
+    _mx_shape(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), names[0])
+    _mx_shape(scales, (rows, cols // 32), names[1])
+
+
+def _mx_rows(x, name):
+    """(rows, cols, pitch) of a 2-D tensor of contiguous rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise TypeError(f"{name}: 2-D tensor of contiguous rows expected (shape [rows, cols], column stride 1)")
+    rows, cols = x.shape
+    pitch = x.stride(0) if rows > 1 else cols
+    if pitch < cols:
+        raise TypeError(f"{name}: rows overlap (shape {list(x.shape)}, row stride {pitch})")
+    return rows, cols, pitch
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise TypeError(f"{name}: CUDA tensor expected")
+
+
+def k3mx_mx_quantize(codes, scales, x, fmt, stream=None):
+    """x [rows, cols] (float32 or bfloat16, rows may be strided) to microscaled
+    codes (uint8 [rows, cols/2] for K3MX_MXFP4, [rows, cols] for K3MX_MXFP8)
+    and scale bytes (uint8 [rows, cols/32])."""
+    rows, cols, pitch = _mx_rows(x, "x")
+    _mx_matrix(codes, scales, rows, cols, fmt)
+    dt = _mx_dtype(x, "x")
+    _dev(codes, torch.uint8, "codes")
+    _dev(scales, torch.uint8, "scales")
+    _cuda(x, "x")
+    _check("k3mx_mx_quantize", lib().k3mx_mx_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows,
+                                                      cols, pitch, fmt, _stream(stream)))
+    return codes, scales
+
+
+def k3mx_mx_dequantize(y, codes, scales, fmt, stream=None):
+    """The values that codes and scale bytes stand for, in y [rows, cols]
+    (float32: exact; bfloat16: rounded to nearest)."""
+    rows, cols, _ = _mx_rows(y, "y")
+    _mx_matrix(codes, scales, rows, cols, fmt)
+    dt = _mx_dtype(y, "y")
+    _dev(y, y.dtype, "y")
+    _dev(codes, torch.uint8, "codes")
+    _dev(scales, torch.uint8, "scales")
+    _check("k3mx_mx_dequantize", lib().k3mx_mx_dequantize(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows,
+                                                          cols, fmt, _stream(stream)))
+    return y
+
+
+def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, stream=None):
+    """sum = x + residual, n = sum * weight / sqrt(mean(sum^2) + eps), codes and
+    scales = n in K3MX_MXFP8, normed (optional, bfloat16) = n.  x [T, width]
+    float32 or bfloat16 (rows may be strided), residual and sum of the same
+    type (both None: no residual; sum may be residual itself), weight
+    bfloat16 [width]."""
+    rows, cols, pitch = _mx_rows(x, "x")
+    _mx_matrix(codes, scales, rows, cols, K3MX_MXFP8)
+    if (residual is None) != (sum is None):
+        raise TypeError("sum: expected exactly where residual is given (shape of x)")
+    for t, n in ((residual, "residual"), (sum, "sum"), (normed, "normed")):
+        if t is not None:
+            _mx_shape(t, (rows, cols), n)
+    _mx_shape(weight, (cols,), "weight")
+    dt = _mx_dtype(x, "x")
+    _dev(codes, torch.uint8, "codes")
+    _dev(scales, torch.uint8, "scales")
+    _cuda(x, "x")
+    _dev_opt(residual, x.dtype, "residual")
+    _dev_opt(sum, x.dtype, "sum")
+    _dev_opt(normed, torch.bfloat16, "normed")
+    _dev(weight, torch.bfloat16, "weight")
+    _check("k3mx_rmsnorm_mx", lib().k3mx_rmsnorm_mx(codes.data_ptr(), scales.data_ptr(), _ptr(sum), _ptr(normed),
+                                                    x.data_ptr(), pitch, _ptr(residual), dt, weight.data_ptr(), eps,
+                                                    rows, cols, _stream(stream)))
+    return codes, scales
+
+
+def _mx_states(y, codes, scales):
+    """(rows, in, out) of a product's activations and output."""
+    rows, inner, _ = _mx_rows(codes, "codes")
+    _mx_matrix(codes, scales, rows, inner, K3MX_MXFP8)
+    if not isinstance(y, torch.Tensor) or y.dim() != 2 or y.shape[0] != rows or y.shape[1] < 1:
+        raise TypeError(f"y: shape [{rows}, out] expected")
+    return rows, inner, y.shape[1]
+
+
+def _mx_product_dev(y, codes, scales, packed, wscales):
+    _dev(y, y.dtype, "y")
+    for t, n in ((codes, "codes"), (scales, "scales"), (packed, "packed"), (wscales, "wscales")):
+        _dev(t, torch.uint8, n)
+
+
+def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
+    """y [T, out] (float32 or bfloat16) = x w^T: x K3MX_MXFP8 (codes [T, in],
+    scales [T, in/32]), w K3MX_MXFP4 (packed [out, in/2], wscales [out, in/32])."""
+    rows, inner, out = _mx_states(y, codes, scales)
+    _mx_matrix(packed, wscales, out, inner, K3MX_MXFP4, ("packed", "wscales"))
+    dt = _mx_dtype(y, "y")
+    _mx_product_dev(y, codes, scales, packed, wscales)
+    _check("k3mx_mx_linear", lib().k3mx_mx_linear(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
+                                                  packed.data_ptr(), wscales.data_ptr(), rows, inner, out,
+                                                  _stream(stream)))
+    return y
+
+
+def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
+    """k3mx_mx_linear by groups: rows offsets[g]:offsets[g+1] (int32 [groups + 1],
+    on the device) with packed[g] [groups, out, in/2], wscales[g]."""
+    rows, inner, out = _mx_states(y, codes, scales)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise TypeError("offsets: shape [groups + 1] expected")
+    groups = offsets.shape[0] - 1
+    _mx_shape(packed, (groups, out, inner // 2), "packed")
+    _mx_shape(wscales, (groups, out, inner // 32), "wscales")
+    dt = _mx_dtype(y, "y")
+    _mx_product_dev(y, codes, scales, packed, wscales)
+    _dev(offsets, torch.int32, "offsets")
+    _check("k3mx_mx_grouped", lib().k3mx_mx_grouped(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
+                                                    packed.data_ptr(), wscales.data_ptr(), offsets.data_ptr(), groups,
+                                                    rows, inner, out, _stream(stream)))
+    return y
 
 
 def k3mx_device_status(stream=None):

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "dense.cuh"
+#include "mxops.cuh"
 #include "prefill.cuh"
 
 namespace k3mx {
@@ -386,6 +387,34 @@ LatentLayout latent_layout(int n_tokens, int h_dtype) {
     return L;
 }
 
+// ------------------------------------------- microscaled operators --
+
+constexpr int64_t kMxMaxPitch = int64_t(1) << 32;       // row pitch of a strided input, in elements
+
+bool mx_shape_ok(int rows, int cols) {
+    return rows >= 1 && rows <= K3MX_MX_MAX_ROWS && cols >= 32 && cols <= K3MX_MX_MAX_COLS && cols % 32 == 0 &&
+           (int64_t)rows * cols <= K3MX_MX_MAX_ELEMENTS;
+}
+
+// the dense and the grouped product: checks, then the launch
+k3mx_status run_mx_product(ProdArgs a, int y_dtype, k3mx_stream_t stream, const char *name) {
+    if (!a.y || !a.codes || !a.scales || !a.packed || !a.wscales) return K3MX_EINVAL;
+    if (y_dtype != K3MX_F32 && y_dtype != K3MX_BF16) return K3MX_EINVAL;
+    if (a.n_rows < 1 || a.n_rows > K3MX_MX_MAX_ROWS || a.out < 1 || a.out > K3MX_MX_MAX_ROWS || a.in < 128 ||
+        a.in > K3MX_MX_MAX_IN || a.in % 128 != 0 || a.n_groups < 1 || a.n_groups > K3MX_MX_MAX_GROUPS ||
+        (int64_t)a.n_groups * a.out > (int64_t(1) << 30))
+        return K3MX_ESHAPE;
+    auto multiple = [](const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+    if (!aligned16(a.y) || !aligned16(a.codes) || !multiple(a.packed, 32) || !multiple(a.scales, 4) ||
+        !multiple(a.wscales, 4) || !multiple(a.offsets, 4))
+        return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    a.status = c.status;
+    return from_cuda(traced(name, c.stream, [&] { return launch_mx_product(c, a, y_dtype == K3MX_BF16); }));
+}
+
 }  // namespace
 }  // namespace k3mx
 
@@ -393,7 +422,7 @@ using namespace k3mx;
 
 extern "C" {
 
-int k3mx_abi_version(void) { return (1 << 16) | 0; }
+int k3mx_abi_version(void) { return (1 << 16) | 1; }
 
 const char *k3mx_last_cuda_error(void) {
     return g_last_cuda == cudaSuccess ? "cudaSuccess" : cudaGetErrorName(g_last_cuda);
@@ -783,6 +812,72 @@ k3mx_status k3mx_moe_routed_host(float *y_host, const void *x_host, int x_dtype,
         cudaStreamSynchronize(s) != cudaSuccess)
         return K3MX_ECUDA;
     return K3MX_OK;
+}
+
+// ------------------------------------- microscaled operators (k3mx_mx.h) --
+
+k3mx_status k3mx_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x_dtype, int rows, int cols,
+                             int64_t ldx, int format, k3mx_stream_t stream) {
+    if (!codes || !scales || !x) return K3MX_EINVAL;
+    if (x_dtype != K3MX_F32 && x_dtype != K3MX_BF16) return K3MX_EINVAL;
+    if (format != K3MX_MXFP4 && format != K3MX_MXFP8) return K3MX_EINVAL;
+    if (!mx_shape_ok(rows, cols) || ldx < cols || ldx > kMxMaxPitch) return K3MX_ESHAPE;
+    const uintptr_t elem = x_dtype == K3MX_BF16 ? 2 : 4;
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(x) & (elem - 1)) != 0) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    return from_cuda(traced("mx_quantize", c.stream, [&] {
+        return launch_mx_quantize(c, codes, scales, x, x_dtype == K3MX_BF16, rows, cols, ldx, format);
+    }));
+}
+
+k3mx_status k3mx_mx_dequantize(void *y, int y_dtype, const uint8_t *codes, const uint8_t *scales, int rows, int cols,
+                               int format, k3mx_stream_t stream) {
+    if (!y || !codes || !scales) return K3MX_EINVAL;
+    if (y_dtype != K3MX_F32 && y_dtype != K3MX_BF16) return K3MX_EINVAL;
+    if (format != K3MX_MXFP4 && format != K3MX_MXFP8) return K3MX_EINVAL;
+    if (!mx_shape_ok(rows, cols)) return K3MX_ESHAPE;
+    if (!aligned16(y) || !aligned16(codes)) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    return from_cuda(traced("mx_dequantize", c.stream, [&] {
+        return launch_mx_dequantize(c, y, y_dtype == K3MX_BF16, codes, scales, rows, cols, format);
+    }));
+}
+
+k3mx_status k3mx_rmsnorm_mx(uint8_t *codes, uint8_t *scales, void *sum, uint16_t *normed, const void *x, int64_t ldx,
+                            const void *residual, int dtype, const uint16_t *g, float eps, int n_tokens, int width,
+                            k3mx_stream_t stream) {
+    if (!codes || !scales || !x || !g || (residual != nullptr) != (sum != nullptr)) return K3MX_EINVAL;
+    if (dtype != K3MX_F32 && dtype != K3MX_BF16) return K3MX_EINVAL;
+    if (!(eps >= 0.f) || eps == INFINITY) return K3MX_EINVAL;
+    if (!mx_shape_ok(n_tokens, width) || width > K3MX_NORM_MAX_WIDTH || ldx < width || ldx > kMxMaxPitch)
+        return K3MX_ESHAPE;
+    const int64_t elem = dtype == K3MX_BF16 ? 2 : 4;
+    if (!aligned16(codes) || !aligned16(x) || !aligned16(g) || !aligned16(residual) || !aligned16(sum) ||
+        !aligned16(normed) || (ldx * elem) % 16 != 0)
+        return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const NormArgs a{codes, scales, sum, normed, x, ldx, residual, g, eps, n_tokens, width};
+    return from_cuda(traced("rmsnorm_mx", c.stream, [&] { return launch_rmsnorm_mx(c, a, dtype == K3MX_BF16); }));
+}
+
+k3mx_status k3mx_mx_linear(void *y, int y_dtype, const uint8_t *codes, const uint8_t *scales, const uint8_t *packed,
+                           const uint8_t *wscales, int n_tokens, int in, int out, k3mx_stream_t stream) {
+    const ProdArgs a{y, codes, scales, packed, wscales, nullptr, 1, n_tokens, in, out, nullptr};
+    return run_mx_product(a, y_dtype, stream, "mx_linear");
+}
+
+k3mx_status k3mx_mx_grouped(void *y, int y_dtype, const uint8_t *codes, const uint8_t *scales, const uint8_t *packed,
+                            const uint8_t *wscales, const int32_t *offsets, int n_groups, int n_rows, int in, int out,
+                            k3mx_stream_t stream) {
+    if (!offsets) return K3MX_EINVAL;
+    const ProdArgs a{y, codes, scales, packed, wscales, offsets, n_groups, n_rows, in, out, nullptr};
+    return run_mx_product(a, y_dtype, stream, "mx_grouped");
 }
 
 k3mx_status k3mx_trace_enable(int on) {
