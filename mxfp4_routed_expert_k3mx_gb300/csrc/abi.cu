@@ -914,7 +914,8 @@ k3mx_status k3mx_set_wait_limit(unsigned int polls) {
     if (st != K3MX_OK) return st;
     const uint32_t p = polls == 0 ? kWaitLimit : (polls > kWaitLimit ? kWaitLimit : polls);
     for (cudaError_t (*set)(uint32_t) : {set_wait_polls_mx, set_wait_polls_px, set_wait_polls_prefill,
-                                         set_wait_polls_decode, set_wait_polls_dense}) {
+                                         set_wait_polls_decode, set_wait_polls_dense,
+                                         set_wait_polls_mxprod}) {
         const cudaError_t e = set(p);
         if (e != cudaSuccess) return from_cuda(e);
     }

@@ -352,6 +352,7 @@ cudaError_t set_wait_polls_px(uint32_t polls);
 cudaError_t set_wait_polls_prefill(uint32_t polls);
 cudaError_t set_wait_polls_decode(uint32_t polls);
 cudaError_t set_wait_polls_dense(uint32_t polls);
+cudaError_t set_wait_polls_mxprod(uint32_t polls);
 
 // Host side.  The library's lazily filled per-device state (device
 // properties, CUDA function attributes, tensor-map templates, the fixed
