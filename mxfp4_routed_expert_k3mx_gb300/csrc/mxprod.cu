@@ -12,15 +12,19 @@
 // width, and the parts meet in shared memory (each CTA adds and stores 128 / S
 // of the outputs, in rank order, so results do not depend on timing).
 // Clusters take items round robin.  Per CTA, the inner width streams in
-// stages of 128 columns:
-//   warp 0      copies: TMA of the weight tile (128 rows x 128 codes, 64 B a
-//               row in memory, spread to 128 B in shared memory, 128-byte
-//               swizzle) and of the unit's rows (boxes of 64 and 16 rows)
-//   warp 1      the tile's scales: four bytes a row and stage, loaded some
-//               stages ahead into registers, stored as the 32-line source of
-//               tcgen05.cp; a block of scale 255 gets scale 0 and its codes
-//               are zeroed once the tile landed, so it adds exactly 0
-//   warp 2      owns TMEM; lane 0 copies scales to TMEM and issues the MMAs
+// tiles of 128 columns, KS tiles to a stage of the ring:
+//   warp 0      copies: one TMA of the stage's weight tiles (128 rows x 128
+//               codes each, 64 B a row in memory, spread to 128 B in shared
+//               memory, 128-byte swizzle), one or a few of the unit's rows
+//   warp 1      the weights' scales, four tiles (16 bytes a row) at a time:
+//               loaded some groups ahead into registers, stored as the 32-line
+//               sources of tcgen05.cp, one fence and one barrier per group; a
+//               block of scale 255 gets scale 0 and its codes are zeroed once
+//               the tile landed, so it adds exactly 0
+//   warp 2      owns TMEM; one elected lane copies scales to TMEM and issues the
+//               MMAs (the whole warp walks the loop, so that addresses and
+//               descriptors stay in uniform registers: with one lane in the
+//               loop, a tile took 1200 clocks to issue whatever its size)
 //   warp 3      the rows' scales, as warp 1's
 //   warps 4-11  epilogue: two warps to a lane quarter, half the rows each
 // Every wait is bounded; one that gives up is reported on the device status
@@ -41,32 +45,43 @@ constexpr int kWTileTx = 128 * 64;         // bytes its copy moves
 constexpr int kAtom = 512;                 // scales of 128 rows and a stage
 constexpr int kThreads = 12 * 32, kEpi0 = 4, kEpiThreads = 8 * 32;
 
+constexpr int kMaxSplit = 8;               // CTAs of a cluster
+
 // outputs of an item that one CTA of a cluster of S adds and stores
 __host__ __device__ constexpr int split_rows(int S) { return S == 3 ? 48 : 128 / S; }
+
+constexpr int kGroup = 4;                  // tiles whose scales travel together
 
 template <int NT_> struct Shape {
     static constexpr int NT = NT_;                                   // rows of a unit
     static constexpr int ATOMS = (NT + 127) / 128;
-    static constexpr int STAGE = kWTile + NT * 128 + (NT == 256 ? 4 : 2) * kAtom;
-    static constexpr int SA = NT == 32 ? 9 : NT == 64 ? 7 : 4;       // stages
+    // Tiles of a stage: two where a unit has few rows, so that what a stage
+    // costs to copy, wait for and issue is spent half as often.
+    static constexpr int KS = NT <= 64 ? 2 : 1;
+    static constexpr int STAGE = KS * (kWTile + NT * 128);
+    static constexpr int SA = NT == 64 ? 3 : 4;                      // stages
+    static constexpr int SG = 3;                                     // scale groups
+    static constexpr int GROUP = kGroup * (1 + ATOMS) * kAtom;       // weights' atoms, then the rows'
     static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators
     static constexpr bool SPLIT = NT < 256;
     // parts of the outputs this CTA adds: [S][NT][split_rows(S)] fp32 (largest at S = 3)
-    static constexpr int RED = SPLIT ? NT * 3 * 48 * 4 : 0;
+    static constexpr int RED = NT == 32 ? NT * 3 * 48 * 4 : NT < 256 ? NT * 128 * 4 : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
-    static constexpr int SMEM = 1024 + 1024 + SA * STAGE + RED + TABLES;
+    static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
     static constexpr int SF_COL = NBUF * NT, SF_STEP = 4 + 4 * ATOMS;  // TMEM columns: accumulators, then scales
     static constexpr int TMEM_COLS = 512;
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
-    static_assert(SF_COL + SA * SF_STEP <= TMEM_COLS, "TMEM");
+    static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
+    static_assert(SA * KS >= kGroup, "a group's weight tiles fit the ring (its dropped blocks are zeroed together)");
 };
 
+// weights, and the rows in boxes of 16, 32 and 64
 struct Maps {
-    CUtensorMap w, x64, x16;
+    CUtensorMap w, x16, x32, x64;
 };
 
 struct Hdr {
-    uint64_t tfull[16], sfull[16], empty[16], accf[2], acce[2], done, redfull, redfree;
+    uint64_t tfull[8], empty[8], gfull[4], gempty[4], accf[2], acce[2], done, redfull, redfree;
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
@@ -106,55 +121,110 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Scale words of a stream of stages: lane l loads the words of rows l, l + 32,
-// ... (R of them) D stages ahead.  begin(i) gives item i's address for the
-// lane's first row and the mask of its rows that exist; use(p, words) takes
-// stage p's.
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// whether the phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// a place in a ring of N slots and the parity of its current use
+template <int N> struct Slot {
+    uint32_t i = 0, ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// Scale words of a stream of items, kcs tiles (words of a row) each, in
+// groups of four tiles: lane l loads the words of rows l, l + 32, ... (R of
+// them) D groups ahead.  begin(i) gives item i's address for the lane's first
+// row and the mask of its rows that exist; use(n, i, c, words) takes the n-th
+// group: tiles c .. c + 3 of item i.  `wide`: rows can be read 16 or 8 bytes
+// at a time (their pitch and first word are so aligned), else word by word.
 template <int R, int D, typename Begin, typename Use>
-__device__ __forceinline__ bool stage_words(int total, int per_item, size_t row_step, Begin begin, Use use) {
-    uint32_t q[D][R];
+__device__ __forceinline__ void scale_groups(int n_items, int kcs, int wide, size_t row_step, Begin begin, Use use) {
+    uint32_t q[D][R][kGroup];
     const uint8_t *base = nullptr;
     uint32_t live = 0;
-    int loaded = 0, c = 0, i = 0;
-    auto load = [&](uint32_t (&d)[R]) {
-        if (loaded >= total) return;
-        if (c == 0) begin(i, base, live);
+    int li = 0, lc = 0;
+    auto load = [&](uint32_t (&d)[R][kGroup]) {
+        if (li >= n_items) return;
+        if (lc == 0) begin(li, base, live);
+        const bool whole = lc + kGroup <= kcs;
 #pragma unroll
-        for (int r = 0; r < R; r++)
-            d[r] = (live >> r) & 1 ? __ldg(reinterpret_cast<const uint32_t *>(base + r * row_step + 4 * c)) : 0u;
-        loaded++;
-        if (++c == per_item) {
-            c = 0;
-            i++;
+        for (int r = 0; r < R; r++) {
+            const uint8_t *at = base + r * row_step + 4 * lc;
+            if (!((live >> r) & 1)) {
+#pragma unroll
+                for (int j = 0; j < kGroup; j++) d[r][j] = 0u;
+            } else if (wide == 16 && whole) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at));
+                d[r][0] = v.x, d[r][1] = v.y, d[r][2] = v.z, d[r][3] = v.w;
+            } else if (wide >= 8 && whole) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at)), w = __ldg(reinterpret_cast<const uint2 *>(at) + 1);
+                d[r][0] = v.x, d[r][1] = v.y, d[r][2] = w.x, d[r][3] = w.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kGroup; j++)
+                    d[r][j] = lc + j < kcs ? __ldg(reinterpret_cast<const uint32_t *>(at) + j) : 0u;
+            }
+        }
+        lc += kGroup;
+        if (lc >= kcs) {
+            lc = 0;
+            li++;
         }
     };
 #pragma unroll
     for (int d = 0; d < D; d++) load(q[d]);
-    for (int p = 0; p < total; p += D) {
+    int n = 0, i = 0, c = 0;
+    while (i < n_items) {
 #pragma unroll
         for (int d = 0; d < D; d++)
-            if (p + d < total) {
-                if (!use(p + d, q[d])) return false;
+            if (i < n_items) {
+                if (!use(n, i, c, q[d])) return;
                 load(q[d]);
+                n++;
+                c += kGroup;
+                if (c >= kcs) {
+                    c = 0;
+                    i++;
+                }
             }
     }
-    return true;
 }
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_constant__ Maps maps) {
+k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, const __grid_constant__ Maps maps) {
     using Sh = Shape<NT>;
-    constexpr int SA = Sh::SA, NBUF = Sh::NBUF;
+    constexpr int SA = Sh::SA, SG = Sh::SG, NBUF = Sh::NBUF, KS = Sh::KS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Hdr *hd = reinterpret_cast<Hdr *>(smem);
     const uint32_t ring = smem_addr(smem) + 1024;
-    float *red = reinterpret_cast<float *>(smem + 1024 + SA * Sh::STAGE);
-    int *ustart = reinterpret_cast<int *>(smem + 1024 + SA * Sh::STAGE + Sh::RED);   // first unit of each group
+    const uint32_t sgroups = ring + SA * Sh::STAGE;
+    float *red = reinterpret_cast<float *>(smem + 1024 + SA * Sh::STAGE + SG * Sh::GROUP);
+    int *ustart = reinterpret_cast<int *>(smem + Sh::SMEM - 1024 - Sh::TABLES);      // first unit of each group
     int *goff = ustart + K3MX_MX_MAX_GROUPS + 8;                                     // first row of each group
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t tfull0 = smem_addr(hd->tfull), sfull0 = smem_addr(hd->sfull), empty0 = smem_addr(hd->empty);
+    const uint32_t tfull0 = smem_addr(hd->tfull), empty0 = smem_addr(hd->empty);
+    const uint32_t gfull0 = smem_addr(hd->gfull), gempty0 = smem_addr(hd->gempty);
     const uint32_t accf0 = smem_addr(hd->accf), acce0 = smem_addr(hd->acce), done = smem_addr(&hd->done);
     const uint32_t redfull = smem_addr(&hd->redfull), redfree = smem_addr(&hd->redfree);
     const int rank = S > 1 ? (int)(blockIdx.x % S) : 0;       // %cluster_ctarank of a 1-D cluster
@@ -162,8 +232,11 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
     if (tid == 0) {
         for (int i = 0; i < SA; i++) {
             mbar_init(tfull0 + 8 * i, 1);
-            mbar_init(sfull0 + 8 * i, 64);
             mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < SG; i++) {
+            mbar_init(gfull0 + 8 * i, 64);
+            mbar_init(gempty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(accf0 + 8 * i, 1);
@@ -219,15 +292,17 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
     if (S > 1) cluster_sync();               // also: every CTA's barriers are initialised
     else __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = hd->tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, hd->tmem, 0);
     volatile int *abort_flag = &hd->abort;
 
     const int MT = (a.out + 127) / 128, KC = a.in / kStageCols, G = a.in / 32;
-    const int c0 = KC * rank / S, kcs = KC * (rank + 1) / S - c0;      // this CTA's stages of every item
+    // this CTA's tiles of every item, whole stages of them
+    const int KF = (KC + KS - 1) / KS, f0 = KF * rank / S, f1 = KF * (rank + 1) / S;
+    const int c0 = f0 * KS, kcs = min(f1 * KS, KC) - c0, fts = f1 - f0;
     const int first = blockIdx.x / S, step = gridDim.x / S;
     const int items = ustart[a.n_groups] * MT;
     const int n_items = items > first ? (items - first + step - 1) / step : 0;
-    const int total = n_items * kcs;
+    const int groups = (kcs + kGroup - 1) / kGroup, n_seg = (groups + seg - 1) / seg;   // accumulations of an item
 
     // item `first + k * step`: groups in order, in a group tile by tile, a
     // tile's units together (they share its weights in L2)
@@ -252,35 +327,42 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
 
     if (warp == 0) {
         // ---------------------------------------------------- copies --
-        if (lane == 0) {
-            const uint64_t wpol = l2_evict_first_policy(), xpol = l2_evict_last_policy();
-            int p = 0;
-            for (int k = 0; k < n_items && !*abort_flag; k++) {
-                const Item it = item_at(k);
-                const int rows = (it.ntok + 15) & ~15, wy = it.g * a.out + it.mt * 128;
-                bool ok = true;
-                for (int c = c0; c < c0 + kcs; c++, p++) {
-                    const int s = p % SA;
-                    if (!mbar_wait(empty0 + 8 * s, ((p / SA) & 1) ^ 1)) {
-                        fail(400);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = ring + s * Sh::STAGE, bar = tfull0 + 8 * s;
-                    mbar_arrive_expect_tx(bar, kWTileTx + rows * 128);
-                    tma_2d(st, &maps.w, c * kStageCols, wy, bar, wpol);
-                    int r = 0;
-                    if (NT >= 64)
-                        for (; r + 64 <= rows; r += 64)
-                            tma_2d(st + kWTile + r * 128, &maps.x64, c * kStageCols, it.off + r, bar, xpol);
-                    for (; r < rows; r += 16)
-                        tma_2d(st + kWTile + r * 128, &maps.x16, c * kStageCols, it.off + r, bar, xpol);
+        const bool leader = elect_one();
+        const uint64_t wpol = l2_evict_first_policy(), xpol = l2_evict_last_policy();
+        Slot<SA> sl;
+        int issued = 0;
+        for (int k = 0; k < n_items && !*abort_flag; k++) {
+            const Item it = item_at(k);
+            const int rows = (it.ntok + 15) & ~15, wy = it.g * a.out + it.mt * 128;
+            const int box = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;          // of the KS = 2 forms
+            const CUtensorMap *xmap = rows <= 16 ? &maps.x16 : rows <= 32 ? &maps.x32 : &maps.x64;
+            bool ok = true;
+            for (int c = c0; c < c0 + kcs; c += KS, issued++, sl.next()) {
+                const uint32_t bar = tfull0 + 8 * sl.i, st = ring + sl.i * Sh::STAGE, xt = st + KS * kWTile;
+                if (!mbar_wait(empty0 + 8 * sl.i, sl.ph ^ 1)) {
+                    if (leader) fail(400);
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
+                if (leader) {
+                    if (KS == 2) {
+                        mbar_arrive_expect_tx(bar, 2 * (kWTileTx + box * 128));
+                        tma_3d(st, &maps.w, 0, wy, c, bar, wpol);
+                        tma_3d(xt, xmap, 0, it.off, c, bar, xpol);
+                    } else {
+                        mbar_arrive_expect_tx(bar, kWTileTx + rows * 128);
+                        tma_3d(st, &maps.w, 0, wy, c, bar, wpol);
+                        int r = 0;
+                        for (; r + 64 <= rows; r += 64) tma_3d(xt + r * 128, &maps.x64, 0, it.off + r, c, bar, xpol);
+                        for (; r < rows; r += 16) tma_3d(xt + r * 128, &maps.x16, 0, it.off + r, c, bar, xpol);
+                    }
+                }
+                __syncwarp();
             }
-            // copies still in flight (after a wait gave up) land before the CTA leaves
-            if (!drain_ring(tfull0, SA, p)) report_status(a.status, kStatusWaitTimeout, 401);
+            if (!ok) break;
         }
+        // copies still in flight (after a wait gave up) land before the CTA leaves
+        if (leader && !drain_ring(tfull0, SA, issued)) report_status(a.status, kStatusWaitTimeout, 401);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------- the tile's scales --
@@ -292,29 +374,38 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
 #pragma unroll
             for (int r = 0; r < 4; r++) live |= (row + 32 * r < a.out ? 1u : 0u) << r;
         };
-        auto use = [&](int p, const uint32_t (&w)[4]) {
-            const int s = p % SA;
-            if (*abort_flag || !mbar_wait(empty0 + 8 * s, ((p / SA) & 1) ^ 1)) {
+        auto use = [&](int n, int i, int c, const uint32_t (&w)[4][kGroup]) {
+            const int gs = n % SG;
+            if (*abort_flag || !mbar_wait(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
                 if (lane == 0) fail(410);
                 return false;
             }
-            const uint32_t st = ring + s * Sh::STAGE;
-            const uint32_t nan = nan_scale_mask(w[0]) | nan_scale_mask(w[1]) | nan_scale_mask(w[2]) | nan_scale_mask(w[3]);
-            if (__any_sync(0xffffffffu, nan != 0)) {        // rare
-                if (!mbar_wait(tfull0 + 8 * s, (p / SA) & 1)) {
-                    if (lane == 0) fail(411);
-                    return false;
-                }
+            uint32_t nan = 0;
 #pragma unroll
-                for (int r = 0; r < 4; r++) zero_nan_groups_x128(st, lane + 32 * r, w[r]);
+            for (int r = 0; r < 4; r++)
+#pragma unroll
+                for (int j = 0; j < kGroup; j++) nan |= nan_scale_mask(w[r][j]);
+            const bool drop = __any_sync(0xffffffffu, nan != 0);        // rare
+#pragma unroll
+            for (int j = 0; j < kGroup; j++) {
+                if (drop && c + j < kcs) {
+                    const int f = i * fts + (c + j) / KS, s = f % SA;
+                    if (!mbar_wait(tfull0 + 8 * s, (f / SA) & 1)) {
+                        if (lane == 0) fail(411);
+                        return false;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; r++) zero_nan_groups_x128(ring + s * Sh::STAGE + (c + j) % KS * kWTile, lane + 32 * r, w[r][j]);
+                }
+                sts128(sgroups + gs * Sh::GROUP + j * kAtom + 16 * lane, drop_nan_scales(w[0][j]),
+                       drop_nan_scales(w[1][j]), drop_nan_scales(w[2][j]), drop_nan_scales(w[3][j]));
             }
-            sts128(st + kWTile + NT * 128 + 16 * lane, drop_nan_scales(w[0]), drop_nan_scales(w[1]),
-                   drop_nan_scales(w[2]), drop_nan_scales(w[3]));
             fence_async_smem();
-            mbar_arrive(sfull0 + 8 * s);
+            mbar_arrive(gfull0 + 8 * gs);
             return true;
         };
-        stage_words<4, 8>(total, kcs, (size_t)32 * G, begin, use);
+        const int wide = (reinterpret_cast<uintptr_t>(a.wscales) | (uintptr_t)G | (uintptr_t)(4 * c0)) & 15;
+        scale_groups<4, 3>(n_items, kcs, wide == 0 ? 16 : wide == 8 ? 8 : 4, (size_t)32 * G, begin, use);
     } else if (warp == 3) {
         // -------------------------------------------- the rows' scales --
         constexpr int R = NT / 32;
@@ -325,71 +416,96 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
 #pragma unroll
             for (int r = 0; r < R; r++) live |= (lane + 32 * r < it.ntok ? 1u : 0u) << r;
         };
-        auto use = [&](int p, const uint32_t (&w)[R]) {
-            const int s = p % SA;
-            if (*abort_flag || !mbar_wait(empty0 + 8 * s, ((p / SA) & 1) ^ 1)) {
+        auto use = [&](int n, int, int, const uint32_t (&w)[R][kGroup]) {
+            const int gs = n % SG;
+            if (*abort_flag || !mbar_wait(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
                 if (lane == 0) fail(420);
                 return false;
             }
-            const uint32_t at = ring + s * Sh::STAGE + kWTile + NT * 128 + kAtom + 16 * lane;
+            const uint32_t at = sgroups + gs * Sh::GROUP + kGroup * kAtom + 16 * lane;
 #pragma unroll
-            for (int r = 0; r < R; r += 4)
-                sts128(at + (r >> 2) * kAtom, w[r], r + 1 < R ? w[r + 1 < R ? r + 1 : 0] : 0u,
-                       r + 2 < R ? w[r + 2 < R ? r + 2 : 0] : 0u, r + 3 < R ? w[r + 3 < R ? r + 3 : 0] : 0u);
+            for (int j = 0; j < kGroup; j++)
+#pragma unroll
+                for (int r = 0; r < R; r += 4)
+                    sts128(at + (j * Sh::ATOMS + (r >> 2)) * kAtom, w[r][j], r + 1 < R ? w[r + 1 < R ? r + 1 : 0][j] : 0u,
+                           r + 2 < R ? w[r + 2 < R ? r + 2 : 0][j] : 0u, r + 3 < R ? w[r + 3 < R ? r + 3 : 0][j] : 0u);
             fence_async_smem();
-            mbar_arrive(sfull0 + 8 * s);
+            mbar_arrive(gfull0 + 8 * gs);
             return true;
         };
-        stage_words<R, NT == 256 ? 4 : 8>(total, kcs, (size_t)32 * G, begin, use);
+        const int wide = (reinterpret_cast<uintptr_t>(a.scales) | (uintptr_t)G | (uintptr_t)(4 * c0)) & 15;
+        scale_groups<R, NT == 256 ? 1 : 3>(n_items, kcs, wide == 0 ? 16 : wide == 8 ? 8 : 4, (size_t)32 * G, begin, use);
     } else if (warp == 2) {
         // ------------------------------------------------ MMA issuer --
-        if (lane == 0) {
-            int p = 0, itn = 0;
-            bool run = true, ready = false;
-            for (int k = 0; k < n_items && run && !*abort_flag; k++, itn++) {
-                const Item it = item_at(k);
-                const int n = (it.ntok + 15) & ~15, b = itn % NBUF;
-                uint32_t idk[4];
-#pragma unroll
-                for (int ks = 0; ks < 4; ks++) idk[ks] = idesc_e2m1_e4m3(n, ks);
-                if (!mbar_wait(acce0 + 8 * b, ((itn / NBUF) & 1) ^ 1)) {
-                    fail(430);
+        const bool leader = elect_one();
+        Slot<SA> sl;
+        Slot<SG> sg;
+        Slot<NBUF> sb;
+        bool run = true, ready = false;                // ready: the next stage's tiles have landed
+        for (int k = 0; k < n_items && run && !*abort_flag; k++) {
+            const int rows = __shfl_sync(0xffffffffu, (item_at(k).ntok + 15) & ~15, 0);
+            const uint32_t xstep = KS == 1 ? 0 : rows <= 16 ? 16 * 128 : rows <= 32 ? 32 * 128 : 64 * 128;
+            const uint32_t id0 = idesc_e2m1_e4m3(rows, 0);
+            int in_seg = 0;
+            for (int c = 0; c < kcs && run; c += kGroup) {
+                if (in_seg == 0 && !mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1)) {
+                    if (leader) fail(430);
+                    run = false;
                     break;
                 }
-                tc_fence_after();
-                for (int c = 0; c < kcs; c++, p++) {
-                    const int s = p % SA, ph = (p / SA) & 1;
-                    if (!ready && (!mbar_wait(tfull0 + 8 * s, ph) || !mbar_wait(sfull0 + 8 * s, ph))) {
-                        fail(431);
+                if (!mbar_wait(gfull0 + 8 * sg.i, sg.ph)) {
+                    if (leader) fail(431);
+                    run = false;
+                    break;
+                }
+                const bool last = c + kGroup >= kcs, seg_end = last || in_seg + 1 == seg;
+                const uint32_t d = tmem + sb.i * NT;
+#pragma unroll
+                for (int j = 0; j < kGroup; j += KS) {
+                    if (c + j >= kcs) break;
+                    if (!ready && !mbar_wait(tfull0 + 8 * sl.i, sl.ph)) {
+                        if (leader) fail(432);
                         run = false;
                         break;
                     }
+                    const Slot<SA> cur = sl;
+                    sl.next();
+                    ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
                     tc_fence_after();
-                    const uint32_t st = ring + s * Sh::STAGE, xt = st + kWTile, sf = xt + NT * 128;
-                    const uint32_t sfa = tmem + Sh::SF_COL + s * Sh::SF_STEP, sfb = sfa + 4;
-                    tmem_cp_atom(sfa, desc_atom(sf, 128));
-                    tmem_cp_atom(sfb, desc_atom(sf + kAtom, 128));
-                    if (Sh::ATOMS == 2 && n > 128) tmem_cp_atom(sfb + 4, desc_atom(sf + 2 * kAtom, 128));
-                    const uint32_t d = tmem + b * NT;
+                    const bool group_end = j + KS >= kGroup || c + j + KS >= kcs;
+                    if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ks++) {
-                        const uint64_t ad = umma_desc_sw128(st + 32 * ks), bd = umma_desc_sw128(xt + 32 * ks);
-                        const uint32_t acc = (c | ks) != 0 ? 1u : 0u;
-                        if (ks == 3) {
-                            // the barriers of the next stage, polled beside the last MMA
-                            const int s2 = (p + 1) % SA, ph2 = ((p + 1) / SA) & 1;
-                            ready = mma_mxf8f6f4_poll3(d, ad, bd, idk[ks], sfa, sfb, acc, tfull0 + 8 * s2, ph2,
-                                                       sfull0 + 8 * s2, ph2, sfull0 + 8 * s2, ph2);
-                        } else {
-                            mma_mxf8f6f4(d, ad, bd, idk[ks], sfa, sfb, acc);
+                        for (int t = 0; t < KS; t++) {
+                            if (t > 0 && c + j + t >= kcs) break;
+                            const uint32_t wt = ring + cur.i * Sh::STAGE + t * kWTile;
+                            const uint32_t xt = ring + cur.i * Sh::STAGE + KS * kWTile + t * xstep;
+                            const uint32_t sf = sgroups + sg.i * Sh::GROUP + (j + t) * kAtom;
+                            const uint32_t sx = sgroups + sg.i * Sh::GROUP + (kGroup + (j + t) * Sh::ATOMS) * kAtom;
+                            const uint32_t sfa = tmem + Sh::SF_COL + (sg.i * kGroup + j + t) * Sh::SF_STEP, sfb = sfa + 4;
+                            tmem_cp_atom(sfa, desc_atom(sf, 128));
+                            tmem_cp_atom(sfb, desc_atom(sx, 128));
+                            if (Sh::ATOMS == 2 && rows > 128) tmem_cp_atom(sfb + 4, desc_atom(sx + kAtom, 128));
+                            const uint64_t ad = umma_desc_sw128(wt), bd = umma_desc_sw128(xt);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ks++)
+                                mma_mxf8f6f4(d, ad + 2 * ks, bd + 2 * ks, id0 | (uint32_t)ks << 4 | (uint32_t)ks << 29, sfa,
+                                             sfb, (in_seg | j | t | ks) != 0 ? 1u : 0u);
                         }
+                        umma_commit(empty0 + 8 * cur.i);
+                        if (group_end) umma_commit(gempty0 + 8 * sg.i);
+                        if (group_end && seg_end) umma_commit(accf0 + 8 * sb.i);
                     }
-                    umma_commit(empty0 + 8 * s);
+                    __syncwarp();
                 }
-                if (run) umma_commit(accf0 + 8 * b);
+                sg.next();
+                in_seg++;
+                if (seg_end) {
+                    in_seg = 0;
+                    sb.next();
+                }
             }
-            umma_commit(done);
         }
+        if (leader) umma_commit(done);
         __syncwarp();
     } else {
         // -------------------------------------------------- epilogue --
@@ -398,26 +514,34 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
         const int o = 32 * q4 + lane;                         // output within the tile
         const uint32_t quarter = (uint32_t)(32 * q4) << 16;
         const int RS = split_rows(S);
+        int an = 0;
         for (int k = 0; k < n_items && !*abort_flag; k++) {
             const Item it = item_at(k);
-            const int b = k % NBUF, n0 = half * HC, n1 = min(it.ntok, n0 + HC);
-            if (!mbar_wait(accf0 + 8 * b, (k / NBUF) & 1)) {
-                if (lane == 0) fail(440);
-                break;
-            }
-            tc_fence_after();
+            const int n0 = half * HC, n1 = min(it.ntok, n0 + HC);
+            // the item's accumulations, added in fp32
             float v[HC];
-#pragma unroll
-            for (int j = 0; j < HC; j += 16)
-                if (n0 + j < n1) {
-                    uint32_t u[16];
-                    tmem_ld16(tmem + quarter + b * NT + n0 + j, u);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; i++) v[j + i] = __uint_as_float(u[i]);
+            bool ok = true;
+            for (int sg = 0; sg < n_seg; sg++, an++) {
+                const int b = an % NBUF;
+                if (!mbar_wait(accf0 + 8 * b, (an / NBUF) & 1)) {
+                    if (lane == 0) fail(440);
+                    ok = false;
+                    break;
                 }
-            tc_fence_before();
-            mbar_arrive(acce0 + 8 * b);
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < HC; j += 16)
+                    if (n0 + j < n1) {
+                        uint32_t u[16];
+                        tmem_ld16(tmem + quarter + b * NT + n0 + j, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) v[j + i] = sg == 0 ? __uint_as_float(u[i]) : v[j + i] + __uint_as_float(u[i]);
+                    }
+                tc_fence_before();
+                mbar_arrive(acce0 + 8 * b);
+            }
+            if (!ok) break;
             auto store = [&](int out, int n, float val) {
                 const size_t at = (size_t)(it.off + n) * a.out + out;
                 if (y_bf16) static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(val);
@@ -474,28 +598,40 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const __grid_const
 
 // ------------------------------------------------------------- launchers --
 
-// packed e2m1 rows: boxes of 128 rows x 128 codes, each 16 packed codes (8
-// bytes) spread over 16 bytes of shared memory
-bool encode_weights(CUtensorMap &m, const void *base, uint64_t cols, uint64_t rows) {
-    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols / 2};
-    const cuuint32_t box[2] = {kStageCols, 128}, es[2] = {1, 1};
-    return tensor_map_encoder()(&m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims, strides,
-                                box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// e4m3 rows: boxes of box_rows rows x 128 columns
-bool encode_states(CUtensorMap &m, const void *base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
-    const cuuint32_t box[2] = {kStageCols, box_rows}, es[2] = {1, 1};
-    return tensor_map_encoder()(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es,
+// Matrices as [tile of 128 columns][row][column]: one copy brings a box of
+// rows of ks neighbouring tiles, each a K-major operand of 128-byte rows.
+bool encode(CUtensorMap &m, CUtensorMapDataType type, const void *base, int in, uint64_t rows, uint64_t pitch,
+            uint64_t tile, uint32_t box_rows, uint32_t ks) {
+    const cuuint64_t dims[3] = {kStageCols, rows, (cuuint64_t)(in / kStageCols)}, strides[2] = {pitch, tile};
+    const cuuint32_t box[3] = {kStageCols, box_rows, ks}, es[3] = {1, 1, 1};
+    return tensor_map_encoder()(&m, type, 3, const_cast<void *>(base), dims, strides, box, es,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// packed e2m1 rows, each 16 packed codes (8 bytes) spread over 16 bytes of
+// shared memory
+bool encode_weights(CUtensorMap &m, const ProdArgs &a, int ks) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, a.packed, a.in, (uint64_t)a.n_groups * a.out, a.in / 2,
+                  kStageCols / 2, 128, ks);
+}
+// e4m3 rows
+bool encode_states(CUtensorMap &m, const ProdArgs &a, int box_rows, int ks) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.in, a.n_rows, a.in, kStageCols, box_rows, ks);
 }
 
+// Scale groups (512 columns) of one accumulation of an fp32 result.  The tensor cores keep fewer
+// bits of a sum than fp32 rounding does: measured at in = 7168, one
+// accumulation of all 56 tiles is 1.5e-6 off (relative, 2-norm) where fp32
+// sums are 3.5e-7 off; two groups keep it below that.
+constexpr int kSegF32 = 2;
+
 template <int NT>
-cudaError_t launch_t(const Ctx &c, const ProdArgs &a, int y_bf16, int S, int clusters, const Maps &maps) {
+cudaError_t launch_t(const Ctx &c, const ProdArgs &a, int y_bf16, int S, int clusters) {
+    constexpr int KS = Shape<NT>::KS;
+    Maps maps;
+    if (!encode_weights(maps.w, a, KS) || !encode_states(maps.x16, a, 16, KS) ||
+        (NT <= 64 && !encode_states(maps.x32, a, 32, KS)) || (NT >= 64 && !encode_states(maps.x64, a, 64, KS)))
+        return cudaErrorInvalidValue;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem((const void *)k_mx_product<NT>, Shape<NT>::SMEM, configured);
     if (e != cudaSuccess) return e;
@@ -512,7 +648,37 @@ cudaError_t launch_t(const Ctx &c, const ProdArgs &a, int y_bf16, int S, int clu
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_mx_product<NT>, a, y_bf16, S, maps);
+    // bf16 results hide what a long accumulation loses in its last bits; fp32
+    // ones are added up from short ones
+    const int seg = y_bf16 ? K3MX_MX_MAX_IN / (kGroup * kStageCols) : kSegF32;
+    return cudaLaunchKernelEx(&cfg, k_mx_product<NT>, a, y_bf16, S, seg, maps);
+}
+
+// Clusters of S CTAs (one CTA an SM) that the device runs at once: an SM's
+// neighbours limit the larger ones.  Asked once per device.
+int resident_clusters(const Ctx &c, int S) {
+    static std::atomic<int> known[64][kMaxSplit + 1];
+    int dev = 0;
+    if (S == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return c.num_sms / S;
+    int n = known[dev][S].load(std::memory_order_relaxed);
+    if (n == 0) {
+        static std::atomic<uint64_t> configured{0};
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(c.num_sms / S * S));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Shape<32>::SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)S;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (ensure_smem((const void *)k_mx_product<32>, Shape<32>::SMEM, configured) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_mx_product<32>, &cfg) != cudaSuccess || n < 1)
+            return 1;
+        known[dev][S].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 struct Plan {
@@ -520,17 +686,21 @@ struct Plan {
 };
 
 // Rows of a unit and CTAs of a cluster.
-Plan choose(const Ctx &c, const ProdArgs &a) {
+Plan choose(const Ctx &c, const ProdArgs &a, int y_bf16) {
     const int groups = a.n_groups < a.n_rows ? a.n_groups : a.n_rows;
     const int mean = (a.n_rows + groups - 1) / groups;       // rows of a group, were they even
     const int MT = (a.out + 127) / 128, KC = a.in / kStageCols;
     Plan best{};
     double least = 0;
     for (int NT : {32, 64, 128, 256}) {
+        const int KS = NT <= 64 ? 2 : 1;
         const long long items = (long long)groups * ((mean + NT - 1) / NT) * MT;
         for (int S : {1, 2, 3, 4, 8}) {
-            if (S > KC || (S > 1 && NT == 256)) continue;
-            long long clusters = c.num_sms / S;
+            // (three parts of 64 or more rows do not fit beside the stages; NT = 256 has
+            // one accumulator, and reading it several times an item would stall the MMAs)
+            if (S > (KC + KS - 1) / KS || (S == 3 && NT > 32)) continue;
+            if (NT == 256 && (S > 1 || (!y_bf16 && KC > kGroup * kSegF32))) continue;
+            long long clusters = resident_clusters(c, S);
             if (clusters > items) clusters = items;
             const long long waves = (items + clusters - 1) / clusters;
             const int n = mean < NT ? (mean + 15) & ~15 : NT;
@@ -553,15 +723,11 @@ cudaError_t launch_mx_product(const Ctx &c, const ProdArgs &a, int y_bf16) {
     if (tensor_map_encoder() == nullptr) return cudaErrorNotSupported;
     const long long units = a.n_rows / 32 + (long long)a.n_groups;
     if (units * ((a.out + 127) / 128) > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    Maps maps;
-    if (!encode_weights(maps.w, a.packed, a.in, (uint64_t)a.n_groups * a.out) ||
-        !encode_states(maps.x64, a.codes, a.in, a.n_rows, 64) || !encode_states(maps.x16, a.codes, a.in, a.n_rows, 16))
-        return cudaErrorInvalidValue;
-    const Plan p = choose(c, a);
-    if (p.NT == 32) return launch_t<32>(c, a, y_bf16, p.S, p.clusters, maps);
-    if (p.NT == 64) return launch_t<64>(c, a, y_bf16, p.S, p.clusters, maps);
-    if (p.NT == 128) return launch_t<128>(c, a, y_bf16, p.S, p.clusters, maps);
-    return launch_t<256>(c, a, y_bf16, p.S, p.clusters, maps);
+    const Plan p = choose(c, a, y_bf16);
+    if (p.NT == 32) return launch_t<32>(c, a, y_bf16, p.S, p.clusters);
+    if (p.NT == 64) return launch_t<64>(c, a, y_bf16, p.S, p.clusters);
+    if (p.NT == 128) return launch_t<128>(c, a, y_bf16, p.S, p.clusters);
+    return launch_t<256>(c, a, y_bf16, p.S, p.clusters);
 }
 
 }  // namespace k3mx
