@@ -125,7 +125,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle alone: the Stream object around it costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -432,31 +433,49 @@ def k3mx_moe_routed_host(y_host, x_host, experts, logits_host, bias_host, worksp
 
 
 # ------------------------------------------------ microscaled operators --
+#
+# One-token calls last a few microseconds on the device, so each function
+# first asks in one expression whether its arguments are as they should be
+# (2 us for six tensors) and names what is wrong only when they are not.
 
 _MX_DTYPES = {torch.float32: K3MX_F32, torch.bfloat16: K3MX_BF16}
+_U8 = torch.uint8
 
 
-def _mx_dtype(t, name):
-    dt = _MX_DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if dt is None:
-        raise TypeError(f"{name}: float32 or bfloat16 tensor expected")
-    return dt
+def _mx_bytes(t, shape):
+    return t.dtype is _U8 and t.shape == shape and t.is_cuda and t.is_contiguous()
 
 
-def _mx_shape(t, shape, name):
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
+def _mx_values(t, shape, dtype):
+    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
+def _mx_need(t, shape, name):
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
         got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
         raise TypeError(f"{name}: shape {list(shape)} expected, got {got}")
 
 
-def _mx_matrix(codes, scales, rows, cols, fmt, names=("codes", "scales")):
-    """Shapes of a microscaled matrix of rows x cols (the sizes a call passes on)."""
+def _mx_refuse(rows, cols, fmt, shapes, bytes_=(), values=(), strided=None):
+    """Raises for the first argument that is not as expected: format and
+    sizes, then shapes, then types and devices.  shapes: (tensor, shape, name);
+    bytes_, values: (tensor, name), values of `strided`'s or their own type."""
     if fmt not in (K3MX_MXFP4, K3MX_MXFP8):
         raise ValueError(f"fmt: K3MX_MXFP4 or K3MX_MXFP8 expected, got {fmt!r}")
     if rows < 1 or cols < 32 or cols % 32:
-        raise TypeError(f"{names[0]}: at least one row and columns in blocks of 32 expected, got {rows} x {cols}")
-    _mx_shape(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), names[0])
-    _mx_shape(scales, (rows, cols // 32), names[1])
+        raise TypeError(f"at least one row and columns in blocks of 32 expected (shape), got {rows} x {cols}")
+    for t, shape, name in shapes:
+        _mx_need(t, shape, name)
+    for t, name in (([strided] if strided else []) + list(values)):
+        if t.dtype not in _MX_DTYPES:
+            raise TypeError(f"{name}: float32 or bfloat16 tensor expected")
+    for t, name in bytes_:
+        _dev(t, _U8, name)
+    for t, name in values:
+        _dev(t, strided[0].dtype if strided else t.dtype, name)
+    if strided and not strided[0].is_cuda:
+        raise TypeError(f"{strided[1]}: CUDA tensor expected")
+    raise TypeError("arguments on different devices, or of unexpected layout")
 
 
 def _mx_rows(x, name):
@@ -470,23 +489,19 @@ def _mx_rows(x, name):
     return rows, cols, pitch
 
 
-def _cuda(t, name):
-    if not t.is_cuda:
-        raise TypeError(f"{name}: CUDA tensor expected")
-
-
 def k3mx_mx_quantize(codes, scales, x, fmt, stream=None):
     """x [rows, cols] (float32 or bfloat16, rows may be strided) to microscaled
     codes (uint8 [rows, cols/2] for K3MX_MXFP4, [rows, cols] for K3MX_MXFP8)
     and scale bytes (uint8 [rows, cols/32])."""
     rows, cols, pitch = _mx_rows(x, "x")
-    _mx_matrix(codes, scales, rows, cols, fmt)
-    dt = _mx_dtype(x, "x")
-    _dev(codes, torch.uint8, "codes")
-    _dev(scales, torch.uint8, "scales")
-    _cuda(x, "x")
-    _check("k3mx_mx_quantize", lib().k3mx_mx_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows,
-                                                      cols, pitch, fmt, _stream(stream)))
+    wide = (rows, cols // 2 if fmt == K3MX_MXFP4 else cols)
+    dt = _MX_DTYPES.get(x.dtype)
+    if not (dt is not None and x.is_cuda and cols % 32 == 0 and _mx_bytes(codes, wide) and
+            _mx_bytes(scales, (rows, cols // 32))):
+        _mx_refuse(rows, cols, fmt, [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales")],
+                   [(codes, "codes"), (scales, "scales")], strided=(x, "x"))
+    _check("k3mx_mx_quantize", (_lib or lib()).k3mx_mx_quantize(
+        codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows, cols, pitch, fmt, _stream(stream)))
     return codes, scales
 
 
@@ -494,13 +509,14 @@ def k3mx_mx_dequantize(y, codes, scales, fmt, stream=None):
     """The values that codes and scale bytes stand for, in y [rows, cols]
     (float32: exact; bfloat16: rounded to nearest)."""
     rows, cols, _ = _mx_rows(y, "y")
-    _mx_matrix(codes, scales, rows, cols, fmt)
-    dt = _mx_dtype(y, "y")
-    _dev(y, y.dtype, "y")
-    _dev(codes, torch.uint8, "codes")
-    _dev(scales, torch.uint8, "scales")
-    _check("k3mx_mx_dequantize", lib().k3mx_mx_dequantize(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows,
-                                                          cols, fmt, _stream(stream)))
+    wide = (rows, cols // 2 if fmt == K3MX_MXFP4 else cols)
+    dt = _MX_DTYPES.get(y.dtype)
+    if not (dt is not None and y.is_cuda and y.is_contiguous() and cols % 32 == 0 and _mx_bytes(codes, wide) and
+            _mx_bytes(scales, (rows, cols // 32))):
+        _mx_refuse(rows, cols, fmt, [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales")],
+                   [(codes, "codes"), (scales, "scales")], [(y, "y")])
+    _check("k3mx_mx_dequantize", (_lib or lib()).k3mx_mx_dequantize(
+        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows, cols, fmt, _stream(stream)))
     return y
 
 
@@ -511,70 +527,74 @@ def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, s
     type (both None: no residual; sum may be residual itself), weight
     bfloat16 [width]."""
     rows, cols, pitch = _mx_rows(x, "x")
-    _mx_matrix(codes, scales, rows, cols, K3MX_MXFP8)
     if (residual is None) != (sum is None):
         raise TypeError("sum: expected exactly where residual is given (shape of x)")
-    for t, n in ((residual, "residual"), (sum, "sum"), (normed, "normed")):
-        if t is not None:
-            _mx_shape(t, (rows, cols), n)
-    _mx_shape(weight, (cols,), "weight")
-    dt = _mx_dtype(x, "x")
-    _dev(codes, torch.uint8, "codes")
-    _dev(scales, torch.uint8, "scales")
-    _cuda(x, "x")
-    _dev_opt(residual, x.dtype, "residual")
-    _dev_opt(sum, x.dtype, "sum")
-    _dev_opt(normed, torch.bfloat16, "normed")
-    _dev(weight, torch.bfloat16, "weight")
-    _check("k3mx_rmsnorm_mx", lib().k3mx_rmsnorm_mx(codes.data_ptr(), scales.data_ptr(), _ptr(sum), _ptr(normed),
-                                                    x.data_ptr(), pitch, _ptr(residual), dt, weight.data_ptr(), eps,
-                                                    rows, cols, _stream(stream)))
+    wide, dt = (rows, cols), _MX_DTYPES.get(x.dtype)
+    if not (dt is not None and x.is_cuda and cols % 32 == 0 and _mx_bytes(codes, wide) and
+            _mx_bytes(scales, (rows, cols // 32)) and _mx_values(weight, (cols,), torch.bfloat16) and
+            (residual is None or (_mx_values(residual, wide, x.dtype) and _mx_values(sum, wide, x.dtype))) and
+            (normed is None or _mx_values(normed, wide, torch.bfloat16))):
+        given = [(t, n) for t, n in ((residual, "residual"), (sum, "sum")) if t is not None]
+        shapes = [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales"), (weight, (cols,), "weight")]
+        if normed is not None:
+            shapes.append((normed, wide, "normed"))
+        for t, shape, n in shapes + [(t, wide, n) for t, n in given]:
+            _mx_need(t, shape, n)
+        _dev(weight, torch.bfloat16, "weight")
+        _dev_opt(normed, torch.bfloat16, "normed")
+        _mx_refuse(rows, cols, K3MX_MXFP8, [], [(codes, "codes"), (scales, "scales")], given, strided=(x, "x"))
+    _check("k3mx_rmsnorm_mx", (_lib or lib()).k3mx_rmsnorm_mx(
+        codes.data_ptr(), scales.data_ptr(), None if sum is None else sum.data_ptr(),
+        None if normed is None else normed.data_ptr(), x.data_ptr(), pitch,
+        None if residual is None else residual.data_ptr(), dt, weight.data_ptr(), eps, rows, cols, _stream(stream)))
     return codes, scales
 
 
-def _mx_states(y, codes, scales):
-    """(rows, in, out) of a product's activations and output."""
-    rows, inner, _ = _mx_rows(codes, "codes")
-    _mx_matrix(codes, scales, rows, inner, K3MX_MXFP8)
+def _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, lead):
+    """lead: () for the dense product, (groups,) for the grouped one."""
+    _mx_need(codes, (rows, inner), "codes")
     if not isinstance(y, torch.Tensor) or y.dim() != 2 or y.shape[0] != rows or y.shape[1] < 1:
         raise TypeError(f"y: shape [{rows}, out] expected")
-    return rows, inner, y.shape[1]
-
-
-def _mx_product_dev(y, codes, scales, packed, wscales):
-    _dev(y, y.dtype, "y")
-    for t, n in ((codes, "codes"), (scales, "scales"), (packed, "packed"), (wscales, "wscales")):
-        _dev(t, torch.uint8, n)
+    out = y.shape[1]
+    _mx_refuse(rows, inner, K3MX_MXFP8,
+               [(scales, (rows, inner // 32), "scales"), (packed, (*lead, out, inner // 2), "packed"),
+                (wscales, (*lead, out, inner // 32), "wscales")],
+               [(codes, "codes"), (scales, "scales"), (packed, "packed"), (wscales, "wscales")], [(y, "y")])
 
 
 def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
     """y [T, out] (float32 or bfloat16) = x w^T: x K3MX_MXFP8 (codes [T, in],
     scales [T, in/32]), w K3MX_MXFP4 (packed [out, in/2], wscales [out, in/32])."""
-    rows, inner, out = _mx_states(y, codes, scales)
-    _mx_matrix(packed, wscales, out, inner, K3MX_MXFP4, ("packed", "wscales"))
-    dt = _mx_dtype(y, "y")
-    _mx_product_dev(y, codes, scales, packed, wscales)
-    _check("k3mx_mx_linear", lib().k3mx_mx_linear(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
-                                                  packed.data_ptr(), wscales.data_ptr(), rows, inner, out,
-                                                  _stream(stream)))
+    rows, inner, _ = _mx_rows(codes, "codes")
+    out, dt = (y.shape[-1] if y.dim() else 0), _MX_DTYPES.get(y.dtype)
+    if not (dt is not None and y.shape == (rows, out) and y.is_cuda and y.is_contiguous() and inner % 32 == 0 and
+            _mx_bytes(codes, (rows, inner)) and _mx_bytes(scales, (rows, inner // 32)) and
+            _mx_bytes(packed, (out, inner // 2)) and _mx_bytes(wscales, (out, inner // 32))):
+        _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, ())
+    _check("k3mx_mx_linear", (_lib or lib()).k3mx_mx_linear(
+        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(), rows, inner,
+        out, _stream(stream)))
     return y
 
 
 def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
     """k3mx_mx_linear by groups: rows offsets[g]:offsets[g+1] (int32 [groups + 1],
     on the device) with packed[g] [groups, out, in/2], wscales[g]."""
-    rows, inner, out = _mx_states(y, codes, scales)
+    rows, inner, _ = _mx_rows(codes, "codes")
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise TypeError("offsets: shape [groups + 1] expected")
     groups = offsets.shape[0] - 1
-    _mx_shape(packed, (groups, out, inner // 2), "packed")
-    _mx_shape(wscales, (groups, out, inner // 32), "wscales")
-    dt = _mx_dtype(y, "y")
-    _mx_product_dev(y, codes, scales, packed, wscales)
-    _dev(offsets, torch.int32, "offsets")
-    _check("k3mx_mx_grouped", lib().k3mx_mx_grouped(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
-                                                    packed.data_ptr(), wscales.data_ptr(), offsets.data_ptr(), groups,
-                                                    rows, inner, out, _stream(stream)))
+    out, dt = (y.shape[-1] if y.dim() else 0), _MX_DTYPES.get(y.dtype)
+    if not (dt is not None and y.shape == (rows, out) and y.is_cuda and y.is_contiguous() and inner % 32 == 0 and
+            _mx_bytes(codes, (rows, inner)) and _mx_bytes(scales, (rows, inner // 32)) and
+            _mx_bytes(packed, (groups, out, inner // 2)) and _mx_bytes(wscales, (groups, out, inner // 32)) and
+            offsets.dtype is torch.int32 and offsets.is_cuda and offsets.is_contiguous()):
+        if all(isinstance(t, torch.Tensor) and t.is_cuda for t in (y, codes, scales, packed, wscales)):
+            _dev(offsets, torch.int32, "offsets")
+        _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, (groups,))
+    _check("k3mx_mx_grouped", (_lib or lib()).k3mx_mx_grouped(
+        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(),
+        offsets.data_ptr(), groups, rows, inner, out, _stream(stream)))
     return y
 
 

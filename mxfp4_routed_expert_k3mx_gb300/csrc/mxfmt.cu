@@ -135,103 +135,144 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], uint8_t *codes, uint8
     return s;
 }
 
+// U runs of eight values a lane, a CTA's threads apart: U loads in flight.
 constexpr int kFmtThreads = 256;
 
-// Eight values a lane.  x rows ldx apart; `per_row` = cols / 8 lanes to a row.
-template <int FMT, bool BF16, bool VEC>
+// x rows ldx apart, `per_row` = cols / 8 runs to a row; FLAT: ldx = cols, so
+// that a run's place needs no division.
+template <int FMT, bool BF16, bool VEC, bool FLAT, int U>
 __global__ void __launch_bounds__(kFmtThreads)
 k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int per_row, int64_t ldx, int *status) {
-    pdl_launch_dependents();
     pdl_wait();
-    const int64_t i = (int64_t)blockIdx.x * kFmtThreads + threadIdx.x;
-    const bool live = i < n8;               // whole blocks: n8 is a multiple of 4
-    const int64_t row = live ? i / per_row : 0;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) load8<BF16, VEC>(x, row * ldx + (i - row * per_row) * 8, v);
-    const uint32_t s = encode8<FMT>(v, codes, scales, i, live);
-    if (FMT == K3MX_MXFP4 && live && s == 255u) report_status(status, kStatusBadIndex, (int)row);
-}
-
-template <int FMT, bool BF16>
-__global__ void __launch_bounds__(kFmtThreads)
-k_mx_dequantize(void *y, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n8) {
     pdl_launch_dependents();
-    pdl_wait();
-    const int64_t i = (int64_t)blockIdx.x * kFmtThreads + threadIdx.x;
-    if (i >= n8) return;
-    const uint32_t s = scales[i >> 2];
-    float v[8];
-    if (FMT == K3MX_MXFP4) {
-        uint32_t h[4];
-        e2m1x8_to_h2x4(reinterpret_cast<const uint32_t *>(codes)[i], h);
-        const float up = s == 255u ? 0.f : e8m0_to_f32(s);
+    const int64_t i0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;
+    float v[U][8];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = h2_to_f2(h[j]);
-            v[2 * j] = f.x * up;
-            v[2 * j + 1] = f.y * up;
-        }
-    } else {
-        const uint2 q = reinterpret_cast<const uint2 *>(codes)[i];
-        const float up = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(s);
+    for (int u = 0; u < U; u++) {
+        const int64_t i = i0 + u * kFmtThreads;       // whole blocks: n8 is a multiple of 4
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const uint32_t pair = (j < 2 ? q.x : q.y) >> (16 * (j & 1));
-            uint32_t h2;
-            asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(pair));
-            const float2 f = h2_to_f2(h2);
-            v[2 * j] = f.x * up;
-            v[2 * j + 1] = f.y * up;
+        for (int j = 0; j < 8; j++) v[u][j] = 0.f;
+        if (i < n8) {
+            int64_t at = 8 * i;
+            if (!FLAT) {
+                // (32-bit division where it is enough)
+                const int64_t row = n8 <= 0x7FFFFFFF ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
+                at = row * ldx + (i - row * per_row) * 8;
+            }
+            load8<BF16, VEC>(x, at, v[u]);
         }
     }
-    store8<BF16>(y, 8 * i, v);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int64_t i = i0 + u * kFmtThreads;
+        const uint32_t s = encode8<FMT>(v[u], codes, scales, i, i < n8);
+        if (FMT == K3MX_MXFP4 && s == 255u && i < n8) report_status(status, kStatusBadIndex, (int)(i / per_row));
+    }
+}
+
+template <int FMT, bool BF16, int U>
+__global__ void __launch_bounds__(kFmtThreads)
+k_mx_dequantize(void *y, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n8) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t i0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;
+    uint2 q[U];
+    uint32_t s[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int64_t i = i0 + u * kFmtThreads;
+        q[u] = make_uint2(0u, 0u);
+        s[u] = 0;
+        if (i < n8) {
+            if (FMT == K3MX_MXFP4) q[u].x = reinterpret_cast<const uint32_t *>(codes)[i];
+            else q[u] = reinterpret_cast<const uint2 *>(codes)[i];
+            s[u] = scales[i >> 2];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int64_t i = i0 + u * kFmtThreads;
+        float v[8];
+        if (FMT == K3MX_MXFP4) {
+            uint32_t h[4];
+            e2m1x8_to_h2x4(q[u].x, h);
+            const float up = s[u] == 255u ? 0.f : e8m0_to_f32(s[u]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 f = h2_to_f2(h[j]);
+                v[2 * j] = f.x * up;
+                v[2 * j + 1] = f.y * up;
+            }
+        } else {
+            const float up = s[u] == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(s[u]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t pair = (j < 2 ? q[u].x : q[u].y) >> (16 * (j & 1));
+                uint32_t h2;
+                asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h2) : "r"(pair));
+                const float2 f = h2_to_f2(h2);
+                v[2 * j] = f.x * up;
+                v[2 * j + 1] = f.y * up;
+            }
+        }
+        if (i < n8) store8<BF16>(y, 8 * i, v);
+    }
 }
 
 // ------------------------------------------------------------------ norm --
 
-// One row per CTA of 1024 threads, the row in registers (8 values a lane and
-// pass, up to 4 passes).
-constexpr int kNormThreads = 1024, kNormVec = 4;
-
-template <bool BF16>
-__global__ void __launch_bounds__(kNormThreads) k_rmsnorm_mx(const NormArgs a) {
-    __shared__ float part[kNormThreads / 32];
-    pdl_launch_dependents();
+// A row to P threads, V passes of 8 values a thread, the row in registers
+// between its two uses (the sum of squares, then the scaled values): every
+// input is read once.  Rows of up to 1024 columns go to one warp each (no
+// barrier), wider ones to one CTA.
+template <int P, int V, bool BF16>
+__global__ void __launch_bounds__(P < 128 ? 128 : P) k_rmsnorm_mx(const NormArgs a) {
+    constexpr int kRows = P < 128 ? 128 / P : 1, kParts = P / 32;
+    __shared__ float part[P < 128 ? 1 : kParts];
     pdl_wait();
-    const int64_t t = blockIdx.x;
-    const int per_row = a.width / 8;
-    float v[kNormVec][8];
+    pdl_launch_dependents();
+    const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / P;
+    const int i0 = threadIdx.x % P, per_row = t < a.n_tokens ? a.width / 8 : 0;
+    float v[V][8];
+    float r[V][8];
+    // every load first
+#pragma unroll
+    for (int p = 0; p < V; p++) {
+        const int i = p * P + i0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[p][j] = r[p][j] = 0.f;
+        if (i < per_row) load8<BF16, true>(a.x, t * a.ldx + 8 * i, v[p]);
+    }
+    if (a.residual != nullptr) {
+#pragma unroll
+        for (int p = 0; p < V; p++)
+            if (p * P + i0 < per_row) load8<BF16, true>(a.residual, t * a.width + 8 * (p * P + i0), r[p]);
+    }
     float ss = 0.f;
 #pragma unroll
-    for (int p = 0; p < kNormVec; p++) {
-        const int i = p * kNormThreads + threadIdx.x;
+    for (int p = 0; p < V; p++) {
+        const int i = p * P + i0;
+        if (a.residual != nullptr && i < per_row) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[p][j] = 0.f;
-        if (i < per_row) {
-            load8<BF16, true>(a.x, t * a.ldx + 8 * i, v[p]);
-            if (a.residual != nullptr) {
-                float r[8];
-                load8<BF16, true>(a.residual, t * a.width + 8 * i, r);
-#pragma unroll
-                for (int j = 0; j < 8; j++) v[p][j] += r[j];
-                store8<BF16>(a.sum, t * a.width + 8 * i, v[p]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; j++) ss = fmaf(v[p][j], v[p][j], ss);
+            for (int j = 0; j < 8; j++) v[p][j] += r[p][j];
+            store8<BF16>(a.sum, t * a.width + 8 * i, v[p]);
         }
+#pragma unroll
+        for (int j = 0; j < 8; j++) ss = fmaf(v[p][j], v[p][j], ss);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    ss = 0.f;
+    if (P > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+        __syncthreads();
+        ss = 0.f;
 #pragma unroll
-    for (int w = 0; w < kNormThreads / 32; w++) ss += part[w];
+        for (int w = 0; w < kParts; w++) ss += part[w];
+    }
     const float k = 1.0f / sqrtf(ss / (float)a.width + a.eps);
 #pragma unroll
-    for (int p = 0; p < kNormVec; p++) {
-        const int i = p * kNormThreads + threadIdx.x;
-        if (p * kNormThreads >= per_row) break;
+    for (int p = 0; p < V; p++) {
+        const int i = p * P + i0;
         const bool live = i < per_row;
         if (live) {
             float g[8];
@@ -244,39 +285,76 @@ __global__ void __launch_bounds__(kNormThreads) k_rmsnorm_mx(const NormArgs a) {
     }
 }
 
+template <int P, int V>
+cudaError_t norm_t(const Ctx &c, const NormArgs &a, int bf16) {
+    constexpr int kRows = P < 128 ? 128 / P : 1;
+    const dim3 grid((unsigned)((a.n_tokens + kRows - 1) / kRows)), block(P < 128 ? 128 : P);
+    return bf16 ? launch_pdl(k_rmsnorm_mx<P, V, true>, grid, block, 0, c.stream, a)
+                : launch_pdl(k_rmsnorm_mx<P, V, false>, grid, block, 0, c.stream, a);
+}
+
 }  // namespace
+
+// Runs a lane: four where that still fills the device several times over.
+// (4096 x 7168 bf16 to MXFP8 and back, us: see the table of measurements.)
+static bool many_runs(const Ctx &c, int64_t n8) { return n8 >= (int64_t)c.num_sms * 8 * kFmtThreads * 4; }
+
+template <int FMT, bool BF16>
+static cudaError_t quantize_t(const Ctx &c, uint8_t *codes, uint8_t *scales, const void *x, int rows, int cols,
+                              int64_t ldx) {
+    const int64_t n8 = (int64_t)rows * cols / 8;
+    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * (BF16 ? 2 : 4)) % 16 == 0;
+    auto go = [&](auto kernel, int U) {
+        const dim3 grid((unsigned)((n8 + kFmtThreads * U - 1) / (kFmtThreads * U)));
+        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, codes, scales, x, n8, cols / 8, ldx, c.status);
+    };
+    if (!vec) return go(k_mx_quantize<FMT, BF16, false, false, 1>, 1);
+    if (ldx != cols) return many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, false, 4>, 4)
+                                             : go(k_mx_quantize<FMT, BF16, true, false, 1>, 1);
+    return many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, true, 4>, 4)
+                            : go(k_mx_quantize<FMT, BF16, true, true, 1>, 1);
+}
 
 cudaError_t launch_mx_quantize(const Ctx &c, uint8_t *codes, uint8_t *scales, const void *x, int x_bf16, int rows,
                                int cols, int64_t ldx, int format) {
+    if (format == K3MX_MXFP4)
+        return x_bf16 ? quantize_t<K3MX_MXFP4, true>(c, codes, scales, x, rows, cols, ldx)
+                      : quantize_t<K3MX_MXFP4, false>(c, codes, scales, x, rows, cols, ldx);
+    return x_bf16 ? quantize_t<K3MX_MXFP8, true>(c, codes, scales, x, rows, cols, ldx)
+                  : quantize_t<K3MX_MXFP8, false>(c, codes, scales, x, rows, cols, ldx);
+}
+
+template <int FMT, bool BF16>
+static cudaError_t dequantize_t(const Ctx &c, void *y, const uint8_t *codes, const uint8_t *scales, int rows, int cols) {
     const int64_t n8 = (int64_t)rows * cols / 8;
-    const dim3 grid((unsigned)((n8 + kFmtThreads - 1) / kFmtThreads));
-    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * (x_bf16 ? 2 : 4)) % 16 == 0;
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, codes, scales, x, n8, cols / 8, ldx, c.status);
+    auto go = [&](auto kernel, int U) {
+        const dim3 grid((unsigned)((n8 + kFmtThreads * U - 1) / (kFmtThreads * U)));
+        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, y, codes, scales, n8);
     };
-    if (format == K3MX_MXFP4) {
-        if (x_bf16) return vec ? go(k_mx_quantize<K3MX_MXFP4, true, true>) : go(k_mx_quantize<K3MX_MXFP4, true, false>);
-        return vec ? go(k_mx_quantize<K3MX_MXFP4, false, true>) : go(k_mx_quantize<K3MX_MXFP4, false, false>);
-    }
-    if (x_bf16) return vec ? go(k_mx_quantize<K3MX_MXFP8, true, true>) : go(k_mx_quantize<K3MX_MXFP8, true, false>);
-    return vec ? go(k_mx_quantize<K3MX_MXFP8, false, true>) : go(k_mx_quantize<K3MX_MXFP8, false, false>);
+    return many_runs(c, n8) ? go(k_mx_dequantize<FMT, BF16, 4>, 4) : go(k_mx_dequantize<FMT, BF16, 1>, 1);
 }
 
 cudaError_t launch_mx_dequantize(const Ctx &c, void *y, int y_bf16, const uint8_t *codes, const uint8_t *scales,
                                  int rows, int cols, int format) {
-    const int64_t n8 = (int64_t)rows * cols / 8;
-    const dim3 grid((unsigned)((n8 + kFmtThreads - 1) / kFmtThreads));
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, y, codes, scales, n8);
-    };
-    if (format == K3MX_MXFP4) return y_bf16 ? go(k_mx_dequantize<K3MX_MXFP4, true>) : go(k_mx_dequantize<K3MX_MXFP4, false>);
-    return y_bf16 ? go(k_mx_dequantize<K3MX_MXFP8, true>) : go(k_mx_dequantize<K3MX_MXFP8, false>);
+    if (format == K3MX_MXFP4)
+        return y_bf16 ? dequantize_t<K3MX_MXFP4, true>(c, y, codes, scales, rows, cols)
+                      : dequantize_t<K3MX_MXFP4, false>(c, y, codes, scales, rows, cols);
+    return y_bf16 ? dequantize_t<K3MX_MXFP8, true>(c, y, codes, scales, rows, cols)
+                  : dequantize_t<K3MX_MXFP8, false>(c, y, codes, scales, rows, cols);
 }
 
 cudaError_t launch_rmsnorm_mx(const Ctx &c, const NormArgs &a, int bf16) {
-    const dim3 grid((unsigned)a.n_tokens);
-    return bf16 ? launch_pdl(k_rmsnorm_mx<true>, grid, dim3(kNormThreads), 0, c.stream, a)
-                : launch_pdl(k_rmsnorm_mx<false>, grid, dim3(kNormThreads), 0, c.stream, a);
+    const int n8 = a.width / 8;
+    if (n8 <= 32) return norm_t<32, 1>(c, a, bf16);
+    if (n8 <= 128) return norm_t<32, 4>(c, a, bf16);
+    // few rows: the fewest values a thread; many: a few warps to a row, so
+    // that several rows share an SM
+    const bool few = a.n_tokens <= c.num_sms;
+    if (n8 <= 256) return few ? norm_t<256, 1>(c, a, bf16) : norm_t<128, 2>(c, a, bf16);
+    if (n8 <= 512) return few ? norm_t<512, 1>(c, a, bf16) : norm_t<128, 4>(c, a, bf16);
+    if (n8 <= 1024) return few ? norm_t<1024, 1>(c, a, bf16) : norm_t<256, 4>(c, a, bf16);
+    if (n8 <= 2048) return norm_t<512, 4>(c, a, bf16);
+    return norm_t<1024, 4>(c, a, bf16);
 }
 
 }  // namespace k3mx

@@ -42,7 +42,7 @@ namespace {
 constexpr int kStageCols = 128;
 constexpr int kWTile = 128 * 128;          // weight tile in shared memory (spread codes)
 constexpr int kWTileTx = 128 * 64;         // bytes its copy moves
-constexpr int kAtom = 512;                 // scales of 128 rows and a stage
+constexpr int kAtom = 512;                 // scales of 128 rows and a tile: 32 lines of 16 bytes
 constexpr int kThreads = 12 * 32, kEpi0 = 4, kEpiThreads = 8 * 32;
 
 constexpr int kMaxSplit = 8;               // CTAs of a cluster
@@ -54,7 +54,7 @@ constexpr int kGroup = 4;                  // tiles whose scales travel together
 
 template <int NT_> struct Shape {
     static constexpr int NT = NT_;                                   // rows of a unit
-    static constexpr int ATOMS = (NT + 127) / 128;
+    static constexpr int ATOMS = NT == 256 ? 2 : 1;                  // the rows' scales of a tile
     // Tiles of a stage: two where a unit has few rows, so that what a stage
     // costs to copy, wait for and issue is spent half as often.
     static constexpr int KS = NT <= 64 ? 2 : 1;
@@ -68,7 +68,9 @@ template <int NT_> struct Shape {
     static constexpr int RED = NT == 32 ? NT * 3 * 48 * 4 : NT < 256 ? NT * 128 * 4 : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
     static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
-    static constexpr int SF_COL = NBUF * NT, SF_STEP = 4 + 4 * ATOMS;  // TMEM columns: accumulators, then scales
+    // TMEM columns: accumulators, then every tile's scales (addresses the MMA
+    // reads scales from are multiples of four columns)
+    static constexpr int SF_COL = NBUF * NT, SF_STEP = 4 + 4 * ATOMS;
     static constexpr int TMEM_COLS = 512;
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
@@ -121,6 +123,15 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// 16 TMEM columns of this warp's lanes; the values are there after
+// tmem_ld_wait (which the compiler may not move their uses ahead of)
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
 // one lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -252,6 +263,8 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     pdl_wait();
     pdl_launch_dependents();
 
+    if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char *>(&maps) + 128 * tid) : "memory");
+
     // units of every group (0 for one whose offsets are unusable)
     constexpr int GPT = (K3MX_MX_MAX_GROUPS + kThreads - 1) / kThreads;
     int nu[GPT], mine = 0;
@@ -331,20 +344,16 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         const uint64_t wpol = l2_evict_first_policy(), xpol = l2_evict_last_policy();
         Slot<SA> sl;
         int issued = 0;
-        for (int k = 0; k < n_items && !*abort_flag; k++) {
+        bool alive = true;                    // as the MMA warp's
+        for (int k = 0; k < n_items; k++) {
             const Item it = item_at(k);
             const int rows = (it.ntok + 15) & ~15, wy = it.g * a.out + it.mt * 128;
             const int box = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;          // of the KS = 2 forms
             const CUtensorMap *xmap = rows <= 16 ? &maps.x16 : rows <= 32 ? &maps.x32 : &maps.x64;
-            bool ok = true;
-            for (int c = c0; c < c0 + kcs; c += KS, issued++, sl.next()) {
+            for (int c = c0; c < c0 + kcs; c += KS, sl.next()) {
                 const uint32_t bar = tfull0 + 8 * sl.i, st = ring + sl.i * Sh::STAGE, xt = st + KS * kWTile;
-                if (!mbar_wait(empty0 + 8 * sl.i, sl.ph ^ 1)) {
-                    if (leader) fail(400);
-                    ok = false;
-                    break;
-                }
-                if (leader) {
+                alive = alive && mbar_wait(empty0 + 8 * sl.i, sl.ph ^ 1);
+                if (leader && alive) {
                     if (KS == 2) {
                         mbar_arrive_expect_tx(bar, 2 * (kWTileTx + box * 128));
                         tma_3d(st, &maps.w, 0, wy, c, bar, wpol);
@@ -356,11 +365,13 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                         for (; r + 64 <= rows; r += 64) tma_3d(xt + r * 128, &maps.x64, 0, it.off + r, c, bar, xpol);
                         for (; r < rows; r += 16) tma_3d(xt + r * 128, &maps.x16, 0, it.off + r, c, bar, xpol);
                     }
+                    issued++;
                 }
                 __syncwarp();
             }
-            if (!ok) break;
+            if (*abort_flag) alive = false;
         }
+        if (leader && !alive) fail(400);
         // copies still in flight (after a wait gave up) land before the CTA leaves
         if (leader && !drain_ring(tfull0, SA, issued)) report_status(a.status, kStatusWaitTimeout, 401);
         __syncwarp();
@@ -423,12 +434,12 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 return false;
             }
             const uint32_t at = sgroups + gs * Sh::GROUP + kGroup * kAtom + 16 * lane;
+            auto word = [&](int r, int j) { return r < R ? w[r < R ? r : 0][j] : 0u; };
 #pragma unroll
             for (int j = 0; j < kGroup; j++)
 #pragma unroll
                 for (int r = 0; r < R; r += 4)
-                    sts128(at + (j * Sh::ATOMS + (r >> 2)) * kAtom, w[r][j], r + 1 < R ? w[r + 1 < R ? r + 1 : 0][j] : 0u,
-                           r + 2 < R ? w[r + 2 < R ? r + 2 : 0][j] : 0u, r + 3 < R ? w[r + 3 < R ? r + 3 : 0][j] : 0u);
+                    sts128(at + (j * Sh::ATOMS + (r >> 2)) * kAtom, w[r][j], word(r + 1, j), word(r + 2, j), word(r + 3, j));
             fence_async_smem();
             mbar_arrive(gfull0 + 8 * gs);
             return true;
@@ -441,62 +452,58 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         Slot<SA> sl;
         Slot<SG> sg;
         Slot<NBUF> sb;
-        bool run = true, ready = false;                // ready: the next stage's tiles have landed
-        for (int k = 0; k < n_items && run && !*abort_flag; k++) {
+        // `alive` turns false when a wait gave up.  The loops run on to their
+        // ends all the same (doing nothing): an exit on a loaded value would
+        // take every address in them out of the uniform registers.
+        bool alive = true, ready = false;              // ready: the next stage's tiles have landed
+        const uint32_t tile_hi = (uint32_t)(umma_desc_sw128(0) >> 32), tile_lo = (uint32_t)umma_desc_sw128(0);
+        const uint32_t atom_hi = (uint32_t)(desc_atom(0, 128) >> 32), atom_lo = (uint32_t)desc_atom(0, 128);
+        auto atom = [&](uint32_t addr16) { return (uint64_t)atom_hi << 32 | (atom_lo + addr16); };
+        auto desc = [&](uint32_t addr16) { return (uint64_t)tile_hi << 32 | (tile_lo + addr16); };
+        for (int k = 0; k < n_items; k++) {
             const int rows = __shfl_sync(0xffffffffu, (item_at(k).ntok + 15) & ~15, 0);
             const uint32_t xstep = KS == 1 ? 0 : rows <= 16 ? 16 * 128 : rows <= 32 ? 32 * 128 : 64 * 128;
-            const uint32_t id0 = idesc_e2m1_e4m3(rows, 0);
+            uint32_t id[4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ks++) id[ks] = idesc_e2m1_e4m3(rows, ks);
             int in_seg = 0;
-            for (int c = 0; c < kcs && run; c += kGroup) {
-                if (in_seg == 0 && !mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1)) {
-                    if (leader) fail(430);
-                    run = false;
-                    break;
-                }
-                if (!mbar_wait(gfull0 + 8 * sg.i, sg.ph)) {
-                    if (leader) fail(431);
-                    run = false;
-                    break;
-                }
+            for (int c = 0; c < kcs; c += kGroup) {
+                if (in_seg == 0) alive = alive && mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1);
+                alive = alive && mbar_wait(gfull0 + 8 * sg.i, sg.ph);
                 const bool last = c + kGroup >= kcs, seg_end = last || in_seg + 1 == seg;
                 const uint32_t d = tmem + sb.i * NT;
+                const uint32_t sf = tmem + Sh::SF_COL + sg.i * (kGroup * Sh::SF_STEP);
+                const uint32_t src = (sgroups + sg.i * Sh::GROUP) >> 4;
 #pragma unroll
-                for (int j = 0; j < kGroup; j += KS) {
-                    if (c + j >= kcs) break;
-                    if (!ready && !mbar_wait(tfull0 + 8 * sl.i, sl.ph)) {
-                        if (leader) fail(432);
-                        run = false;
-                        break;
-                    }
-                    const Slot<SA> cur = sl;
-                    sl.next();
-                    ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
-                    tc_fence_after();
-                    const bool group_end = j + KS >= kGroup || c + j + KS >= kcs;
-                    if (leader) {
+                for (int j = 0; j < kGroup; j += KS)
+                    if (c + j < kcs) {
+                        alive = alive && (ready || mbar_wait(tfull0 + 8 * sl.i, sl.ph));
+                        const uint32_t slot = sl.i, wt = (ring + slot * Sh::STAGE) >> 4;
+                        sl.next();
+                        ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
+                        tc_fence_after();
+                        const bool group_end = j + KS >= kGroup || c + j + KS >= kcs;
+                        if (leader && alive) {
 #pragma unroll
-                        for (int t = 0; t < KS; t++) {
-                            if (t > 0 && c + j + t >= kcs) break;
-                            const uint32_t wt = ring + cur.i * Sh::STAGE + t * kWTile;
-                            const uint32_t xt = ring + cur.i * Sh::STAGE + KS * kWTile + t * xstep;
-                            const uint32_t sf = sgroups + sg.i * Sh::GROUP + (j + t) * kAtom;
-                            const uint32_t sx = sgroups + sg.i * Sh::GROUP + (kGroup + (j + t) * Sh::ATOMS) * kAtom;
-                            const uint32_t sfa = tmem + Sh::SF_COL + (sg.i * kGroup + j + t) * Sh::SF_STEP, sfb = sfa + 4;
-                            tmem_cp_atom(sfa, desc_atom(sf, 128));
-                            tmem_cp_atom(sfb, desc_atom(sx, 128));
-                            if (Sh::ATOMS == 2 && rows > 128) tmem_cp_atom(sfb + 4, desc_atom(sx + kAtom, 128));
-                            const uint64_t ad = umma_desc_sw128(wt), bd = umma_desc_sw128(xt);
+                            for (int t = 0; t < KS; t++)
+                                if (t == 0 || c + j + t < kcs) {
+                                    const uint32_t sfa = sf + (j + t) * Sh::SF_STEP, sfb = sfa + 4;
+                                    tmem_cp_atom(sfa, atom(src + (j + t) * (kAtom >> 4)));
+                                    tmem_cp_atom(sfb, atom(src + (kGroup + (j + t) * Sh::ATOMS) * (kAtom >> 4)));
+                                    if (Sh::ATOMS == 2 && rows > 128)
+                                        tmem_cp_atom(sfb + 4, atom(src + (kGroup + (j + t) * Sh::ATOMS + 1) * (kAtom >> 4)));
+                                    const uint32_t ad = wt + t * (kWTile >> 4), bd = wt + ((KS * kWTile + t * xstep) >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ks++)
-                                mma_mxf8f6f4(d, ad + 2 * ks, bd + 2 * ks, id0 | (uint32_t)ks << 4 | (uint32_t)ks << 29, sfa,
-                                             sfb, (in_seg | j | t | ks) != 0 ? 1u : 0u);
+                                    for (int ks = 0; ks < 4; ks++)
+                                        mma_mxf8f6f4(d, desc(ad + 2 * ks), desc(bd + 2 * ks), id[ks], sfa, sfb,
+                                                     (in_seg | j | t | ks) != 0 ? 1u : 0u);
+                                }
+                            umma_commit(empty0 + 8 * slot);
+                            if (group_end) umma_commit(gempty0 + 8 * sg.i);
+                            if (group_end && seg_end) umma_commit(accf0 + 8 * sb.i);
                         }
-                        umma_commit(empty0 + 8 * cur.i);
-                        if (group_end) umma_commit(gempty0 + 8 * sg.i);
-                        if (group_end && seg_end) umma_commit(accf0 + 8 * sb.i);
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
                 sg.next();
                 in_seg++;
                 if (seg_end) {
@@ -504,7 +511,9 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     sb.next();
                 }
             }
+            if (*abort_flag) alive = false;
         }
+        if (leader && !alive) fail(430);
         if (leader) umma_commit(done);
         __syncwarp();
     } else {
@@ -514,33 +523,41 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         const int o = 32 * q4 + lane;                         // output within the tile
         const uint32_t quarter = (uint32_t)(32 * q4) << 16;
         const int RS = split_rows(S);
-        int an = 0;
+        Slot<NBUF> sb;
         for (int k = 0; k < n_items && !*abort_flag; k++) {
             const Item it = item_at(k);
             const int n0 = half * HC, n1 = min(it.ntok, n0 + HC);
-            // the item's accumulations, added in fp32
+            // The item's accumulations, added in fp32.  The first is loaded
+            // whole (rows past the unit's hold whatever was there) and waited
+            // for once.
             float v[HC];
-            bool ok = true;
-            for (int sg = 0; sg < n_seg; sg++, an++) {
-                const int b = an % NBUF;
-                if (!mbar_wait(accf0 + 8 * b, (an / NBUF) & 1)) {
-                    if (lane == 0) fail(440);
-                    ok = false;
-                    break;
-                }
+            bool ok = mbar_wait(accf0 + 8 * sb.i, sb.ph);
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(acce0 + 8 * sb.i);
+                sb.next();
+            }
+            for (int sg = 1; sg < n_seg && ok; sg++, sb.next()) {
+                ok = mbar_wait(accf0 + 8 * sb.i, sb.ph);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < HC; j += 16)
                     if (n0 + j < n1) {
-                        uint32_t u[16];
-                        tmem_ld16(tmem + quarter + b * NT + n0 + j, u);
+                        float u[16];
+                        tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, u);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; i++) v[j + i] = sg == 0 ? __uint_as_float(u[i]) : v[j + i] + __uint_as_float(u[i]);
+                        for (int i = 0; i < 16; i++) v[j + i] += u[i];
                     }
                 tc_fence_before();
-                mbar_arrive(acce0 + 8 * b);
+                mbar_arrive(acce0 + 8 * sb.i);
             }
+            if (!ok && lane == 0) fail(440);
             if (!ok) break;
             auto store = [&](int out, int n, float val) {
                 const size_t at = (size_t)(it.off + n) * a.out + out;
