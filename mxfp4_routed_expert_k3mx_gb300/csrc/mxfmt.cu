@@ -48,15 +48,27 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// 8 consecutive values a lane, neighbouring lanes neighbouring runs, both of a
+// pair live or neither; whole warps.  fp32: the lanes of a pair swap halves,
+// so that each store instruction writes whole 32-byte sectors.
 template <bool BF16>
-__device__ __forceinline__ void store8(void *base, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void *base, int64_t i, const float (&v)[8], bool live) {
     if (BF16) {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + i) =
+        if (live) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + i) =
             make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
     } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        const bool odd = threadIdx.x & 1;
+        float4 t;
+        t.x = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[4], 1);
+        t.y = __shfl_xor_sync(0xffffffffu, odd ? v[1] : v[5], 1);
+        t.z = __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[6], 1);
+        t.w = __shfl_xor_sync(0xffffffffu, odd ? v[3] : v[7], 1);
+        // even: own first half and the neighbour's, odd: the neighbour's second half and its own
+        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + (odd ? i - 8 : i));
+        if (live) {
+            p[odd ? 1 : 0] = odd ? t : make_float4(v[0], v[1], v[2], v[3]);
+            p[odd ? 3 : 2] = odd ? make_float4(v[4], v[5], v[6], v[7]) : t;
+        }
     }
 }
 
@@ -146,6 +158,9 @@ k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int pe
     pdl_wait();
     pdl_launch_dependents();
     const int64_t i0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;
+    // the CTA's first run: one division a CTA
+    const int64_t row0 = FLAT ? 0 : (i0 - threadIdx.x) / per_row;
+    const int col0 = FLAT ? 0 : (int)(i0 - threadIdx.x - row0 * per_row);
     float v[U][8];
 #pragma unroll
     for (int u = 0; u < U; u++) {
@@ -155,9 +170,18 @@ k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int pe
         if (i < n8) {
             int64_t at = 8 * i;
             if (!FLAT) {
-                // (32-bit division where it is enough)
-                const int64_t row = n8 <= 0x7FFFFFFF ? (int64_t)((uint32_t)i / (uint32_t)per_row) : i / per_row;
-                at = row * ldx + (i - row * per_row) * 8;
+                int64_t r = row0;
+                int c = col0 + (int)threadIdx.x + u * kFmtThreads;
+                if (per_row >= kFmtThreads) {          // at most U rows on
+                    while (c >= per_row) {
+                        c -= per_row;
+                        r++;
+                    }
+                } else {
+                    r += c / per_row;
+                    c %= per_row;
+                }
+                at = r * ldx + c * 8;
             }
             load8<BF16, VEC>(x, at, v[u]);
         }
@@ -215,59 +239,60 @@ k_mx_dequantize(void *y, const uint8_t *__restrict__ codes, const uint8_t *__res
                 v[2 * j + 1] = f.y * up;
             }
         }
-        if (i < n8) store8<BF16>(y, 8 * i, v);
+        store8<BF16>(y, 8 * i, v, i < n8);
     }
 }
 
 // ------------------------------------------------------------------ norm --
 
-// A row to P threads, V passes of 8 values a thread, the row in registers
-// between its two uses (the sum of squares, then the scaled values): every
-// input is read once.  Rows of up to 1024 columns go to one warp each (no
-// barrier), wider ones to one CTA.
-template <int P, int V, bool BF16>
-__global__ void __launch_bounds__(P < 128 ? 128 : P) k_rmsnorm_mx(const NormArgs a) {
-    constexpr int kRows = P < 128 ? 128 / P : 1, kParts = P / 32;
-    __shared__ float part[P < 128 ? 1 : kParts];
+// V runs of 8 values a thread, the row in registers between its two uses (the
+// sum of squares, then the scaled values): every input is read once, all
+// loads of a row at the start.  WARP: a row to a warp, four rows to a CTA of
+// 128 threads, no barrier; else a row to a CTA of as many warps as its runs
+// need.
+template <bool WARP, int V, bool BF16>
+__global__ void __launch_bounds__(WARP ? 128 : V == 1 ? 1024 : V == 2 ? 512 : 1024) k_rmsnorm_mx(const NormArgs a) {
+    __shared__ float part[32];
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / P;
-    const int i0 = threadIdx.x % P, per_row = t < a.n_tokens ? a.width / 8 : 0;
+    const int lane = threadIdx.x & 31, P = WARP ? 32 : blockDim.x;
+    const int64_t t = WARP ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    const int i0 = WARP ? lane : threadIdx.x, per_row = t < a.n_tokens ? a.width / 8 : 0;
     float v[V][8];
-    float r[V][8];
-    // every load first
 #pragma unroll
     for (int p = 0; p < V; p++) {
-        const int i = p * P + i0;
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[p][j] = r[p][j] = 0.f;
-        if (i < per_row) load8<BF16, true>(a.x, t * a.ldx + 8 * i, v[p]);
+        for (int j = 0; j < 8; j++) v[p][j] = 0.f;
+        if (p * P + i0 < per_row) load8<BF16, true>(a.x, t * a.ldx + 8 * (p * P + i0), v[p]);
     }
     if (a.residual != nullptr) {
+        float r[V][8];
 #pragma unroll
-        for (int p = 0; p < V; p++)
+        for (int p = 0; p < V; p++) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) r[p][j] = 0.f;
             if (p * P + i0 < per_row) load8<BF16, true>(a.residual, t * a.width + 8 * (p * P + i0), r[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < V; p++) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[p][j] += r[p][j];
+            store8<BF16>(a.sum, t * a.width + 8 * (p * P + i0), v[p], p * P + i0 < per_row);
+        }
     }
     float ss = 0.f;
 #pragma unroll
-    for (int p = 0; p < V; p++) {
-        const int i = p * P + i0;
-        if (a.residual != nullptr && i < per_row) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[p][j] += r[p][j];
-            store8<BF16>(a.sum, t * a.width + 8 * i, v[p]);
-        }
+    for (int p = 0; p < V; p++)
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(v[p][j], v[p][j], ss);
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (P > 32) {
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+    if (!WARP) {
+        if (lane == 0) part[threadIdx.x >> 5] = ss;
         __syncthreads();
-        ss = 0.f;
+        ss = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
 #pragma unroll
-        for (int w = 0; w < kParts; w++) ss += part[w];
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
     const float k = 1.0f / sqrtf(ss / (float)a.width + a.eps);
 #pragma unroll
@@ -279,18 +304,18 @@ __global__ void __launch_bounds__(P < 128 ? 128 : P) k_rmsnorm_mx(const NormArgs
             load8<true, true>(a.g, 8 * i, g);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[p][j] = v[p][j] * k * g[j];
-            if (a.normed != nullptr) store8<true>(a.normed, t * a.width + 8 * i, v[p]);
+            if (a.normed != nullptr) store8<true>(a.normed, t * a.width + 8 * i, v[p], true);
         }
         encode8<K3MX_MXFP8>(v[p], a.codes, a.scales, t * per_row + i, live);
     }
 }
 
-template <int P, int V>
+template <bool WARP, int V>
 cudaError_t norm_t(const Ctx &c, const NormArgs &a, int bf16) {
-    constexpr int kRows = P < 128 ? 128 / P : 1;
-    const dim3 grid((unsigned)((a.n_tokens + kRows - 1) / kRows)), block(P < 128 ? 128 : P);
-    return bf16 ? launch_pdl(k_rmsnorm_mx<P, V, true>, grid, block, 0, c.stream, a)
-                : launch_pdl(k_rmsnorm_mx<P, V, false>, grid, block, 0, c.stream, a);
+    const int warps = WARP ? 4 : (a.width / 8 + 32 * V - 1) / (32 * V);
+    const dim3 grid((unsigned)(WARP ? (a.n_tokens + 3) / 4 : a.n_tokens)), block(32 * warps);
+    return bf16 ? launch_pdl(k_rmsnorm_mx<WARP, V, true>, grid, block, 0, c.stream, a)
+                : launch_pdl(k_rmsnorm_mx<WARP, V, false>, grid, block, 0, c.stream, a);
 }
 
 }  // namespace
@@ -345,16 +370,12 @@ cudaError_t launch_mx_dequantize(const Ctx &c, void *y, int y_bf16, const uint8_
 
 cudaError_t launch_rmsnorm_mx(const Ctx &c, const NormArgs &a, int bf16) {
     const int n8 = a.width / 8;
-    if (n8 <= 32) return norm_t<32, 1>(c, a, bf16);
-    if (n8 <= 128) return norm_t<32, 4>(c, a, bf16);
-    // few rows: the fewest values a thread; many: a few warps to a row, so
-    // that several rows share an SM
-    const bool few = a.n_tokens <= c.num_sms;
-    if (n8 <= 256) return few ? norm_t<256, 1>(c, a, bf16) : norm_t<128, 2>(c, a, bf16);
-    if (n8 <= 512) return few ? norm_t<512, 1>(c, a, bf16) : norm_t<128, 4>(c, a, bf16);
-    if (n8 <= 1024) return few ? norm_t<1024, 1>(c, a, bf16) : norm_t<256, 4>(c, a, bf16);
-    if (n8 <= 2048) return norm_t<512, 4>(c, a, bf16);
-    return norm_t<1024, 4>(c, a, bf16);
+    if (n8 <= 32) return norm_t<true, 1>(c, a, bf16);
+    if (n8 <= 128) return norm_t<true, 4>(c, a, bf16);
+    // few rows: the fewest values a thread; many: two runs a thread, so that
+    // several rows share an SM
+    if (n8 <= 1024) return a.n_tokens <= c.num_sms ? norm_t<false, 1>(c, a, bf16) : norm_t<false, 2>(c, a, bf16);
+    return norm_t<false, 4>(c, a, bf16);
 }
 
 }  // namespace k3mx

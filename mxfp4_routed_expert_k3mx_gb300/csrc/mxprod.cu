@@ -45,10 +45,13 @@ constexpr int kWTileTx = 128 * 64;         // bytes its copy moves
 constexpr int kAtom = 512;                 // scales of 128 rows and a tile: 32 lines of 16 bytes
 constexpr int kThreads = 12 * 32, kEpi0 = 4, kEpiThreads = 8 * 32;
 
-constexpr int kMaxSplit = 8;               // CTAs of a cluster
+constexpr int kMaxSplit = 8;               // CTAs of a cluster: 1, 2, 4 or 8
 
-// outputs of an item that one CTA of a cluster of S adds and stores
-__host__ __device__ constexpr int split_rows(int S) { return S == 3 ? 48 : 128 / S; }
+// One exchange of a cluster: kExCols rows of the unit, every CTA's parts of
+// this CTA's 128 / S outputs, [part][output][row] fp32.  Outputs lie kExPitch
+// apart, so that 16-byte accesses of neighbouring outputs hit different banks.
+constexpr int kExCols = 32, kExPitch = kExCols + 4;
+constexpr int kExBytes = 128 * kExPitch * 4;
 
 constexpr int kGroup = 4;                  // tiles whose scales travel together
 
@@ -59,13 +62,12 @@ template <int NT_> struct Shape {
     // costs to copy, wait for and issue is spent half as often.
     static constexpr int KS = NT <= 64 ? 2 : 1;
     static constexpr int STAGE = KS * (kWTile + NT * 128);
-    static constexpr int SA = NT == 64 ? 3 : 4;                      // stages
+    static constexpr int SA = NT == 64 ? 3 : NT == 128 ? 5 : 4;      // stages
     static constexpr int SG = 3;                                     // scale groups
     static constexpr int GROUP = kGroup * (1 + ATOMS) * kAtom;       // weights' atoms, then the rows'
     static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators
     static constexpr bool SPLIT = NT < 256;
-    // parts of the outputs this CTA adds: [S][NT][split_rows(S)] fp32 (largest at S = 3)
-    static constexpr int RED = NT == 32 ? NT * 3 * 48 * 4 : NT < 256 ? NT * 128 * 4 : 0;
+    static constexpr int RED = SPLIT ? 2 * kExBytes : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
     static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
     // TMEM columns: accumulators, then every tile's scales (addresses the MMA
@@ -83,7 +85,7 @@ struct Maps {
 };
 
 struct Hdr {
-    uint64_t tfull[8], empty[8], gfull[4], gempty[4], accf[2], acce[2], done, redfull, redfree;
+    uint64_t tfull[8], empty[8], gfull[4], gempty[4], accf[2], acce[2], done, exfull[2];
     uint32_t tmem;
     int abort;
     int part[kThreads / 32];
@@ -98,11 +100,11 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// 16 bytes into another CTA's shared memory; the bytes count on its barrier
+__device__ __forceinline__ void st_async4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
     const uint32_t lim = wait_polls();
@@ -230,14 +232,14 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     Hdr *hd = reinterpret_cast<Hdr *>(smem);
     const uint32_t ring = smem_addr(smem) + 1024;
     const uint32_t sgroups = ring + SA * Sh::STAGE;
-    float *red = reinterpret_cast<float *>(smem + 1024 + SA * Sh::STAGE + SG * Sh::GROUP);
+    uint8_t *red = smem + 1024 + SA * Sh::STAGE + SG * Sh::GROUP;
     int *ustart = reinterpret_cast<int *>(smem + Sh::SMEM - 1024 - Sh::TABLES);      // first unit of each group
     int *goff = ustart + K3MX_MX_MAX_GROUPS + 8;                                     // first row of each group
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t tfull0 = smem_addr(hd->tfull), empty0 = smem_addr(hd->empty);
     const uint32_t gfull0 = smem_addr(hd->gfull), gempty0 = smem_addr(hd->gempty);
     const uint32_t accf0 = smem_addr(hd->accf), acce0 = smem_addr(hd->acce), done = smem_addr(&hd->done);
-    const uint32_t redfull = smem_addr(&hd->redfull), redfree = smem_addr(&hd->redfree);
+    const uint32_t exfull0 = smem_addr(hd->exfull);
     const int rank = S > 1 ? (int)(blockIdx.x % S) : 0;       // %cluster_ctarank of a 1-D cluster
 
     if (tid == 0) {
@@ -254,8 +256,8 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             mbar_init(acce0 + 8 * i, kEpiThreads);
         }
         mbar_init(done, 1);
-        mbar_init(redfull, S * (kEpiThreads / 32));
-        mbar_init(redfree, S * (kEpiThreads / 32));
+        mbar_init(exfull0, 1);
+        mbar_init(exfull0 + 8, 1);
         hd->abort = 0;
         fence_mbar_init();
     }
@@ -522,28 +524,29 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         const int q4 = warp & 3, half = (warp - kEpi0) >> 2;
         const int o = 32 * q4 + lane;                         // output within the tile
         const uint32_t quarter = (uint32_t)(32 * q4) << 16;
-        const int RS = split_rows(S);
+        const int RS = 128 / S;                               // outputs this CTA adds
         Slot<NBUF> sb;
-        for (int k = 0; k < n_items && !*abort_flag; k++) {
+        Slot<2> ex;
+        // `alive` as in the MMA warp: the loops run to their ends, so the named
+        // barrier below always has all its warps
+        bool alive = true;
+        for (int k = 0; k < n_items; k++) {
             const Item it = item_at(k);
             const int n0 = half * HC, n1 = min(it.ntok, n0 + HC);
             // The item's accumulations, added in fp32.  The first is loaded
             // whole (rows past the unit's hold whatever was there) and waited
             // for once.
             float v[HC];
-            bool ok = mbar_wait(accf0 + 8 * sb.i, sb.ph);
+            alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
             tc_fence_after();
-            if (ok) {
 #pragma unroll
-                for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
-                tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(acce0 + 8 * sb.i);
-                sb.next();
-            }
-            for (int sg = 1; sg < n_seg && ok; sg++, sb.next()) {
-                ok = mbar_wait(accf0 + 8 * sb.i, sb.ph);
-                if (!ok) break;
+            for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(acce0 + 8 * sb.i);
+            sb.next();
+            for (int sg = 1; sg < n_seg; sg++, sb.next()) {
+                alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < HC; j += 16)
@@ -557,8 +560,6 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 tc_fence_before();
                 mbar_arrive(acce0 + 8 * sb.i);
             }
-            if (!ok && lane == 0) fail(440);
-            if (!ok) break;
             auto store = [&](int out, int n, float val) {
                 const size_t at = (size_t)(it.off + n) * a.out + out;
                 if (y_bf16) static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(val);
@@ -566,40 +567,58 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             };
             if (!Sh::SPLIT || S == 1) {
                 const int out = it.mt * 128 + o;
-                if (out < a.out)
+                if (out < a.out && alive)
 #pragma unroll
                     for (int j = 0; j < HC; j++)
                         if (n0 + j < n1) store(out, n0 + j, v[j]);
-                continue;
-            }
-            // this CTA's parts to the CTAs that add them, once those are done
-            // with the item before
-            if (k > 0 && !wait_cluster(redfree, (k - 1) & 1)) {
-                if (lane == 0) fail(441);
-                break;
-            }
-            {
+            } else {
+                // Exchanges of kExCols rows.  Every CTA sends its parts of all
+                // outputs to the CTAs that add them.  A buffer is used again two
+                // exchanges later: by then this CTA has all parts of the exchange
+                // between, and no CTA sends those before all its warps (the
+                // named barrier) are done with the one before.
                 const int own = o / RS;
-                const uint32_t to = map_rank(smem_addr(red) + ((rank * NT + n0) * RS + o - own * RS) * 4, own);
 #pragma unroll
-                for (int j = 0; j < HC; j++)
-                    if (n0 + j < n1) st_cluster(to + j * RS * 4, v[j]);
+                for (int x = 0; x < NT / kExCols; x++) {
+                    if (x * kExCols >= it.ntok) break;
+                    const int cols = (min(kExCols, it.ntok - x * kExCols) + 3) & ~3;
+                    const uint32_t buf = smem_addr(red) + ex.i * kExBytes, bar = exfull0 + 8 * ex.i;
+                    named_sync(1, kEpiThreads);
+                    if (warp == kEpi0 && lane == 0) mbar_arrive_expect_tx(bar, S * RS * cols * 16 / 4);
+                    const uint32_t to = map_rank(buf + (rank * RS + o - own * RS) * (kExPitch * 4), own), tobar = map_rank(bar, own);
+                    constexpr int PER = HC < kExCols ? HC : kExCols;             // this warp's rows of an exchange
+                    if (HC < kExCols || x / (HC / PER) == half) {
+#pragma unroll
+                        for (int j = 0; j < PER; j += 4) {
+                            const int jj = HC < kExCols ? j : (x % (HC / PER)) * PER + j;      // in v
+                            const int n = HC < kExCols ? n0 + j : j;                           // of the exchange
+                            if (n < cols) st_async4(to + n * 4, v[jj], v[jj + 1], v[jj + 2], v[jj + 3], tobar);
+                        }
+                    }
+                    alive = alive && wait_cluster(bar, ex.ph);
+                    const float *src = reinterpret_cast<const float *>(red + ex.i * kExBytes);
+                    for (int i = tid - kEpi0 * 32; i < RS * (cols / 4); i += kEpiThreads) {
+                        const int n = i / RS * 4, r = i % RS, out = it.mt * 128 + rank * RS + r;
+                        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int s = 0; s < S; s++) {
+                            const float4 q = *reinterpret_cast<const float4 *>(src + (s * RS + r) * kExPitch + n);
+                            sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
+                        }
+                        const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+                        if (out < a.out && alive)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                if (x * kExCols + n + j < it.ntok) store(out, x * kExCols + n + j, f[j]);
+                    }
+                    ex.next();
+                }
             }
-            __syncwarp();
-            if (lane < S) arrive_cluster(map_rank(redfull, lane));
-            if (!wait_cluster(redfull, k & 1)) {
-                if (lane == 0) fail(442);
-                break;
-            }
-            const int cnt = min(RS, 128 - rank * RS);
-            for (int i = tid - kEpi0 * 32; i < cnt * it.ntok; i += kEpiThreads) {
-                const int n = i / cnt, r = i - n * cnt, out = it.mt * 128 + rank * RS + r;
-                float sum = 0.f;
-                for (int s = 0; s < S; s++) sum += red[(s * NT + n) * RS + r];
-                if (out < a.out) store(out, n, sum);
-            }
-            __syncwarp();
-            if (lane < S) arrive_cluster(map_rank(redfree, lane));
+            if (*abort_flag) alive = false;
+        }
+        if (!alive) {
+            if (lane == 0) fail(440);
+            // parts of others may still be under way to this CTA
+            for (int i = 0; S > 1 && i < 100; i++) __nanosleep(1000);
         }
     }
 
@@ -712,10 +731,10 @@ Plan choose(const Ctx &c, const ProdArgs &a, int y_bf16) {
     for (int NT : {32, 64, 128, 256}) {
         const int KS = NT <= 64 ? 2 : 1;
         const long long items = (long long)groups * ((mean + NT - 1) / NT) * MT;
-        for (int S : {1, 2, 3, 4, 8}) {
-            // (three parts of 64 or more rows do not fit beside the stages; NT = 256 has
-            // one accumulator, and reading it several times an item would stall the MMAs)
-            if (S > (KC + KS - 1) / KS || (S == 3 && NT > 32)) continue;
+        for (int S : {1, 2, 4, 8}) {
+            // (NT = 256 has one accumulator: reading it several times an item would
+            // stall the MMAs)
+            if (S > (KC + KS - 1) / KS) continue;
             if (NT == 256 && (S > 1 || (!y_bf16 && KC > kGroup * kSegF32))) continue;
             long long clusters = resident_clusters(c, S);
             if (clusters > items) clusters = items;
