@@ -62,11 +62,11 @@ template <int NT_> struct Shape {
     // costs to copy, wait for and issue is spent half as often.
     static constexpr int KS = NT <= 64 ? 2 : 1;
     static constexpr int STAGE = KS * (kWTile + NT * 128);
-    static constexpr int SA = NT == 64 ? 3 : NT == 128 ? 5 : 4;      // stages
+    static constexpr int SA = NT == 64 ? 3 : NT == 128 ? 6 : 4;      // stages
     static constexpr int SG = 3;                                     // scale groups
     static constexpr int GROUP = kGroup * (1 + ATOMS) * kAtom;       // weights' atoms, then the rows'
     static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators
-    static constexpr bool SPLIT = NT < 256;
+    static constexpr bool SPLIT = NT <= 64;                          // clusters of more than one CTA
     static constexpr int RED = SPLIT ? 2 * kExBytes : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
     static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
@@ -139,6 +139,13 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
     return p != 0;
+}
+__device__ __forceinline__ void tma_prefetch_3d(const void *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 // whether the phase has completed, without waiting
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -262,59 +269,82 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         fence_mbar_init();
     }
     if (warp == 2) tmem_alloc(smem_addr(&hd->tmem), Sh::TMEM_COLS);
-    pdl_wait();
-    pdl_launch_dependents();
-
-    if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char *>(&maps) + 128 * tid) : "memory");
-
-    // units of every group (0 for one whose offsets are unusable)
-    constexpr int GPT = (K3MX_MX_MAX_GROUPS + kThreads - 1) / kThreads;
-    int nu[GPT], mine = 0;
-#pragma unroll
-    for (int k = 0; k < GPT; k++) {
-        const int g = tid * GPT + k;
-        nu[k] = 0;
-        if (g < a.n_groups) {
-            const int lo = a.offsets ? __ldg(a.offsets + g) : 0, hi = a.offsets ? __ldg(a.offsets + g + 1) : a.n_rows;
-            if (lo < 0 || hi < lo || hi > a.n_rows) {
-                if (blockIdx.x == 0) report_status(a.status, kStatusBadIndex, g);
-            } else {
-                nu[k] = (hi - lo + NT - 1) / NT;
-            }
-            goff[g] = lo;
-            if (g == a.n_groups - 1) goff[a.n_groups] = hi;
-        }
-        mine += nu[k];
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) hd->part[warp] = incl;
-    __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < warp; w++) at += hd->part[w];
-#pragma unroll
-    for (int k = 0; k < GPT; k++) {
-        const int g = tid * GPT + k;
-        if (g < a.n_groups) ustart[g] = at;
-        at += nu[k];
-        if (g == a.n_groups - 1) ustart[a.n_groups] = at;
-    }
-    tc_fence_before();
-    if (S > 1) cluster_sync();               // also: every CTA's barriers are initialised
-    else __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, hd->tmem, 0);
-    volatile int *abort_flag = &hd->abort;
-
+    if (tid < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<const char *>(&maps) + 128 * tid) : "memory");
     const int MT = (a.out + 127) / 128, KC = a.in / kStageCols, G = a.in / 32;
     // this CTA's tiles of every item, whole stages of them
     const int KF = (KC + KS - 1) / KS, f0 = KF * rank / S, f1 = KF * (rank + 1) / S;
     const int c0 = f0 * KS, kcs = min(f1 * KS, KC) - c0, fts = f1 - f0;
     const int first = blockIdx.x / S, step = gridDim.x / S;
+    pdl_launch_dependents();
+    if (a.offsets == nullptr) {
+        // One group of all rows: everything up to the copies is ready before
+        // the kernel before this one ends, and the first weights are on their
+        // way into L2 (they may be that kernel's output: L2 is where it writes).
+        if (tid == 0) {
+            ustart[0] = goff[0] = 0;
+            ustart[1] = (a.n_rows + NT - 1) / NT;
+            goff[1] = a.n_rows;
+        }
+        const int mt = first / ((a.n_rows + NT - 1) / NT);
+        if (mt < MT) {
+            if (warp == 0 && lane < SA && lane * KS < kcs)
+                tma_prefetch_3d(&maps.w, 0, mt * 128, c0 + lane * KS);
+            if (warp == 1)
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    if (mt * 128 + lane + 32 * r < a.out)
+                        prefetch_l2(a.wscales + (size_t)(mt * 128 + lane + 32 * r) * G + 4 * c0);
+        }
+    } else {
+        pdl_wait();
+        // units of every group (0 for one whose offsets are unusable)
+        constexpr int GPT = (K3MX_MX_MAX_GROUPS + kThreads - 1) / kThreads;
+        int nu[GPT], mine = 0;
+#pragma unroll
+        for (int k = 0; k < GPT; k++) {
+            const int g = tid * GPT + k;
+            nu[k] = 0;
+            if (g < a.n_groups) {
+                const int lo = __ldg(a.offsets + g), hi = __ldg(a.offsets + g + 1);
+                if (lo < 0 || hi < lo || hi > a.n_rows) {
+                    if (blockIdx.x == 0) report_status(a.status, kStatusBadIndex, g);
+                } else {
+                    nu[k] = (hi - lo + NT - 1) / NT;
+                }
+                goff[g] = lo;
+                if (g == a.n_groups - 1) goff[a.n_groups] = hi;
+            }
+            mine += nu[k];
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) hd->part[warp] = incl;
+        __syncthreads();
+        int before = lane < warp ? hd->part[lane] : 0;                 // (12 warps)
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        int at = __shfl_sync(0xffffffffu, before, 0) + incl - mine;
+#pragma unroll
+        for (int k = 0; k < GPT; k++) {
+            const int g = tid * GPT + k;
+            if (g < a.n_groups) ustart[g] = at;
+            at += nu[k];
+            if (g == a.n_groups - 1) ustart[a.n_groups] = at;
+        }
+    }
+    tc_fence_before();
+    if (S > 1) cluster_sync();               // also: every CTA's barriers are initialised
+    else __syncthreads();
+    tc_fence_after();
+    if (a.offsets == nullptr) pdl_wait();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, hd->tmem, 0);
+    volatile int *abort_flag = &hd->abort;
+
     const int items = ustart[a.n_groups] * MT;
     const int n_items = items > first ? (items - first + step - 1) / step : 0;
     const int groups = (kcs + kGroup - 1) / kGroup, n_seg = (groups + seg - 1) / seg;   // accumulations of an item
@@ -322,18 +352,18 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     // item `first + k * step`: groups in order, in a group tile by tile, a
     // tile's units together (they share its weights in L2)
     auto item_at = [&](int k) {
-        const int it = first + k * step, q = it / MT;
+        const uint32_t it = first + k * step, q = it / (uint32_t)MT;
         int lo = 0, hi = a.n_groups - 1;                    // last group with ustart <= q
         while (lo < hi) {
             const int m = (lo + hi + 1) >> 1;
-            if (ustart[m] <= q) lo = m;
+            if (ustart[m] <= (int)q) lo = m;
             else hi = m - 1;
         }
-        const int u0 = ustart[lo], ug = ustart[lo + 1] - u0, l = it - u0 * MT;
-        const int mt = l / ug, u = l - mt * ug;
-        const long long cnt = goff[lo + 1] - goff[lo];
-        const int r0 = (int)(cnt * u / ug), r1 = (int)(cnt * (u + 1) / ug);
-        return Item{lo, mt, goff[lo] + r0, r1 - r0};
+        const uint32_t u0 = ustart[lo], ug = ustart[lo + 1] - u0, l = it - u0 * MT;
+        const uint32_t mt = l / ug, u = l - mt * ug;
+        // the group's rows in ug units, the first ones a row longer
+        const uint32_t cnt = goff[lo + 1] - goff[lo], each = cnt / ug, more = cnt - each * ug;
+        return Item{lo, (int)mt, goff[lo] + (int)(each * u + min(u, more)), (int)(each + (u < more ? 1 : 0))};
     };
     auto fail = [&](int detail) {
         report_status(a.status, kStatusWaitTimeout, detail);
@@ -560,17 +590,22 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 tc_fence_before();
                 mbar_arrive(acce0 + 8 * sb.i);
             }
-            auto store = [&](int out, int n, float val) {
-                const size_t at = (size_t)(it.off + n) * a.out + out;
-                if (y_bf16) static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(val);
-                else static_cast<float *>(a.y)[at] = val;
-            };
             if (!Sh::SPLIT || S == 1) {
                 const int out = it.mt * 128 + o;
-                if (out < a.out && alive)
+                if (out < a.out && alive) {
+                    const size_t at = (size_t)(it.off + n0) * a.out + out;
+                    if (y_bf16) {
+                        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + at;
 #pragma unroll
-                    for (int j = 0; j < HC; j++)
-                        if (n0 + j < n1) store(out, n0 + j, v[j]);
+                        for (int j = 0; j < HC; j++, y += a.out)
+                            if (n0 + j < n1) *y = __float2bfloat16_rn(v[j]);
+                    } else {
+                        float *y = static_cast<float *>(a.y) + at;
+#pragma unroll
+                        for (int j = 0; j < HC; j++, y += a.out)
+                            if (n0 + j < n1) *y = v[j];
+                    }
+                }
             } else {
                 // Exchanges of kExCols rows.  Every CTA sends its parts of all
                 // outputs to the CTAs that add them.  A buffer is used again two
@@ -605,10 +640,19 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                             sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
                         }
                         const float f[4] = {sum.x, sum.y, sum.z, sum.w};
-                        if (out < a.out && alive)
+                        const int left = it.ntok - x * kExCols - n;
+                        if (out < a.out && alive) {
+                            const size_t at = (size_t)(it.off + x * kExCols + n) * a.out + out;
+                            if (y_bf16) {
 #pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                if (x * kExCols + n + j < it.ntok) store(out, x * kExCols + n + j, f[j]);
+                                for (int j = 0; j < 4; j++)
+                                    if (j < left) static_cast<__nv_bfloat16 *>(a.y)[at + (size_t)j * a.out] = __float2bfloat16_rn(f[j]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; j++)
+                                    if (j < left) static_cast<float *>(a.y)[at + (size_t)j * a.out] = f[j];
+                            }
+                        }
                     }
                     ex.next();
                 }
@@ -735,7 +779,7 @@ Plan choose(const Ctx &c, const ProdArgs &a, int y_bf16) {
             // (NT = 256 has one accumulator: reading it several times an item would
             // stall the MMAs)
             if (S > (KC + KS - 1) / KS) continue;
-            if (NT == 256 && (S > 1 || (!y_bf16 && KC > kGroup * kSegF32))) continue;
+            if ((S > 1 && NT > 64) || (NT == 256 && !y_bf16 && KC > kGroup * kSegF32)) continue;
             long long clusters = resident_clusters(c, S);
             if (clusters > items) clusters = items;
             const long long waves = (items + clusters - 1) / clusters;
