@@ -43,7 +43,7 @@ constexpr int kStageCols = 128;
 constexpr int kWTile = 128 * 128;          // weight tile in shared memory (spread codes)
 constexpr int kWTileTx = 128 * 64;         // bytes its copy moves
 constexpr int kAtom = 512;                 // scales of 128 rows and a tile: 32 lines of 16 bytes
-constexpr int kThreads = 12 * 32, kEpi0 = 4, kEpiThreads = 8 * 32;
+constexpr int kEpi0 = 4, kEpiThreads = 8 * 32, kIssuer1 = 12;   // warps; see the head of this file
 
 constexpr int kMaxSplit = 8;               // CTAs of a cluster: 1, 2, 4 or 8
 
@@ -65,14 +65,19 @@ template <int NT_> struct Shape {
     static constexpr int SA = NT == 64 ? 3 : NT == 128 ? 6 : 4;      // stages
     static constexpr int SG = 3;                                     // scale groups
     static constexpr int GROUP = kGroup * (1 + ATOMS) * kAtom;       // weights' atoms, then the rows'
-    static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators
+    // Warps that issue MMAs, the stages of an item dealt among them, each with
+    // accumulators of its own (the epilogue adds them): one's waits and
+    // address work overlap the other's MMAs.
+    static constexpr int ISS = NT <= 64 ? 2 : 1;
+    static constexpr int THREADS = ISS == 2 ? 13 * 32 : 12 * 32;
+    static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators of an issuer
     static constexpr bool SPLIT = NT <= 64;                          // clusters of more than one CTA
     static constexpr int RED = SPLIT ? 2 * kExBytes : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
     static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
     // TMEM columns: accumulators, then every tile's scales (addresses the MMA
     // reads scales from are multiples of four columns)
-    static constexpr int SF_COL = NBUF * NT, SF_STEP = 4 + 4 * ATOMS;
+    static constexpr int SF_COL = ISS * NBUF * NT, SF_STEP = 4 + 4 * ATOMS;
     static constexpr int TMEM_COLS = 512;
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
@@ -88,7 +93,7 @@ struct Hdr {
     uint64_t tfull[8], empty[8], gfull[4], gempty[4], accf[2], acce[2], done, exfull[2];
     uint32_t tmem;
     int abort;
-    int part[kThreads / 32];
+    int part[16];
 };
 
 struct Item {
@@ -168,72 +173,83 @@ template <int N> struct Slot {
             ph ^= 1;
         }
     }
+    __device__ __forceinline__ void add(uint32_t n) {          // n <= 2 N
+        for (i += n; i >= N; i -= N) ph ^= 1;
+    }
 };
+
+// loads that happen or leave their registers alone (a predicate and no branch)
+__device__ __forceinline__ void ldg_if(uint32_t &v, const uint8_t *p, bool live) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(p), "r"((uint32_t)live));
+}
+__device__ __forceinline__ void ldg2_if(uint32_t &v, uint32_t &w, const uint8_t *p, bool live) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+                 : "+r"(v), "+r"(w) : "l"(p), "r"((uint32_t)live));
+}
 
 // Scale words of a stream of items, kcs tiles (words of a row) each, in
 // groups of four tiles: lane l loads the words of rows l, l + 32, ... (R of
-// them) D groups ahead.  begin(i) gives item i's address for the lane's first
-// row and the mask of its rows that exist; use(n, i, c, words) takes the n-th
-// group: tiles c .. c + 3 of item i.  `wide`: rows can be read 16 or 8 bytes
-// at a time (their pitch and first word are so aligned), else word by word.
-template <int R, int D, typename Begin, typename Use>
-__device__ __forceinline__ void scale_groups(int n_items, int kcs, int wide, size_t row_step, Begin begin, Use use) {
-    uint32_t q[D][R][kGroup];
-    const uint8_t *base = nullptr;
-    uint32_t live = 0;
-    int li = 0, lc = 0;
-    auto load = [&](uint32_t (&d)[R][kGroup]) {
-        if (li >= n_items) return;
-        if (lc == 0) begin(li, base, live);
-        const bool whole = lc + kGroup <= kcs;
+// them), W bytes at a time, a group ahead of its use (two or three ahead cost
+// more, in code to fetch and in loads before the first use, than they hid:
+// 1 x 3584 x 7168 8.0 us, 8.5 and 10.0).  begin(i, base) gives item i's first
+// words of the lane's R rows (rows that do not exist repeat one that does);
+// use(n, i, c, words) takes the n-th group: tiles c .. c + 3 of item i (words
+// past the item's last tile are any that were loaded before).  A load has one
+// width and no alternative, so that it is not waited for before its use: with
+// a branch between widths, the moves at its end waited for each.
+template <int R, int W, typename Begin, typename Use>
+__device__ __forceinline__ void scale_groups_w(int n_items, int kcs, Begin begin, Use use) {
+    uint32_t q[R][kGroup];
+    const uint8_t *base[R];
+    auto load = [&](int i, int c) {
+        if (c == 0) begin(i, base);
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            const uint8_t *at = base + r * row_step + 4 * lc;
-            if (!((live >> r) & 1)) {
-#pragma unroll
-                for (int j = 0; j < kGroup; j++) d[r][j] = 0u;
-            } else if (wide == 16 && whole) {
+            const uint8_t *at = base[r] + 4 * c;
+            if (W == 16) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at));
-                d[r][0] = v.x, d[r][1] = v.y, d[r][2] = v.z, d[r][3] = v.w;
-            } else if (wide >= 8 && whole) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at)), w = __ldg(reinterpret_cast<const uint2 *>(at) + 1);
-                d[r][0] = v.x, d[r][1] = v.y, d[r][2] = w.x, d[r][3] = w.y;
+                q[r][0] = v.x, q[r][1] = v.y, q[r][2] = v.z, q[r][3] = v.w;
+            } else if (W == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+                q[r][0] = v.x, q[r][1] = v.y;
+                ldg2_if(q[r][2], q[r][3], at + 8, c + 2 < kcs);
             } else {
 #pragma unroll
-                for (int j = 0; j < kGroup; j++)
-                    d[r][j] = lc + j < kcs ? __ldg(reinterpret_cast<const uint32_t *>(at) + j) : 0u;
+                for (int j = 0; j < kGroup; j++) ldg_if(q[r][j], at + 4 * j, c + j < kcs);
             }
-        }
-        lc += kGroup;
-        if (lc >= kcs) {
-            lc = 0;
-            li++;
         }
     };
 #pragma unroll
-    for (int d = 0; d < D; d++) load(q[d]);
-    int n = 0, i = 0, c = 0;
-    while (i < n_items) {
+    for (int r = 0; r < R; r++)
 #pragma unroll
-        for (int d = 0; d < D; d++)
-            if (i < n_items) {
-                if (!use(n, i, c, q[d])) return;
-                load(q[d]);
-                n++;
-                c += kGroup;
-                if (c >= kcs) {
-                    c = 0;
-                    i++;
-                }
-            }
+        for (int j = 0; j < kGroup; j++) q[r][j] = 0u;
+    int n = 0, i = 0, c = 0;
+    if (n_items > 0) load(0, 0);
+    while (i < n_items) {
+        if (!use(n, i, c, q)) return;
+        n++;
+        c += kGroup;
+        if (c >= kcs) {
+            c = 0;
+            i++;
+        }
+        if (i < n_items) load(i, c);
     }
+}
+// W by what the first words' addresses (`bits`: their low bits) and the
+// items' length allow
+template <int R, typename Begin, typename Use>
+__device__ __forceinline__ void scale_groups(int n_items, int kcs, uint32_t bits, Begin begin, Use use) {
+    if ((bits & 15) == 0 && kcs % 4 == 0) scale_groups_w<R, 16>(n_items, kcs, begin, use);
+    else if ((bits & 7) == 0 && kcs % 2 == 0) scale_groups_w<R, 8>(n_items, kcs, begin, use);
+    else scale_groups_w<R, 4>(n_items, kcs, begin, use);
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
 k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, const __grid_constant__ Maps maps) {
     using Sh = Shape<NT>;
-    constexpr int SA = Sh::SA, SG = Sh::SG, NBUF = Sh::NBUF, KS = Sh::KS;
+    constexpr int SA = Sh::SA, SG = Sh::SG, NBUF = Sh::NBUF, KS = Sh::KS, ISS = Sh::ISS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Hdr *hd = reinterpret_cast<Hdr *>(smem);
@@ -256,13 +272,13 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         }
         for (int i = 0; i < SG; i++) {
             mbar_init(gfull0 + 8 * i, 64);
-            mbar_init(gempty0 + 8 * i, 1);
+            mbar_init(gempty0 + 8 * i, ISS);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(accf0 + 8 * i, 1);
+            mbar_init(accf0 + 8 * i, ISS);
             mbar_init(acce0 + 8 * i, kEpiThreads);
         }
-        mbar_init(done, 1);
+        mbar_init(done, ISS);
         mbar_init(exfull0, 1);
         mbar_init(exfull0 + 8, 1);
         hd->abort = 0;
@@ -299,13 +315,13 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     } else {
         pdl_wait();
         // units of every group (0 for one whose offsets are unusable)
-        constexpr int GPT = (K3MX_MX_MAX_GROUPS + kThreads - 1) / kThreads;
+        constexpr int GPT = (K3MX_MX_MAX_GROUPS + 383) / 384;        // groups a thread (12 warps)
         int nu[GPT], mine = 0;
 #pragma unroll
         for (int k = 0; k < GPT; k++) {
             const int g = tid * GPT + k;
             nu[k] = 0;
-            if (g < a.n_groups) {
+            if (g < a.n_groups && tid < 384) {
                 const int lo = __ldg(a.offsets + g), hi = __ldg(a.offsets + g + 1);
                 if (lo < 0 || hi < lo || hi > a.n_rows) {
                     if (blockIdx.x == 0) report_status(a.status, kStatusBadIndex, g);
@@ -332,6 +348,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
         for (int k = 0; k < GPT; k++) {
             const int g = tid * GPT + k;
+            if (tid >= 384) break;
             if (g < a.n_groups) ustart[g] = at;
             at += nu[k];
             if (g == a.n_groups - 1) ustart[a.n_groups] = at;
@@ -409,13 +426,11 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------- the tile's scales --
-        auto begin = [&](int k, const uint8_t *&base, uint32_t &live) {
+        auto begin = [&](int k, const uint8_t *(&base)[4]) {
             const Item it = item_at(k);
-            const int row = it.mt * 128 + lane;
-            base = a.wscales + ((size_t)it.g * a.out + row) * G + 4 * c0;
-            live = 0;
 #pragma unroll
-            for (int r = 0; r < 4; r++) live |= (row + 32 * r < a.out ? 1u : 0u) << r;
+            for (int r = 0; r < 4; r++)
+                base[r] = a.wscales + ((size_t)it.g * a.out + min(it.mt * 128 + lane + 32 * r, a.out - 1)) * G + 4 * c0;
         };
         auto use = [&](int n, int i, int c, const uint32_t (&w)[4][kGroup]) {
             const int gs = n % SG;
@@ -447,17 +462,15 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             mbar_arrive(gfull0 + 8 * gs);
             return true;
         };
-        const int wide = (reinterpret_cast<uintptr_t>(a.wscales) | (uintptr_t)G | (uintptr_t)(4 * c0)) & 15;
-        scale_groups<4, 3>(n_items, kcs, wide == 0 ? 16 : wide == 8 ? 8 : 4, (size_t)32 * G, begin, use);
+        scale_groups<4>(n_items, kcs, (uint32_t)reinterpret_cast<uintptr_t>(a.wscales) | G | 4 * c0, begin, use);
     } else if (warp == 3) {
         // -------------------------------------------- the rows' scales --
         constexpr int R = NT / 32;
-        auto begin = [&](int k, const uint8_t *&base, uint32_t &live) {
+        auto begin = [&](int k, const uint8_t *(&base)[R]) {
             const Item it = item_at(k);
-            base = a.scales + ((size_t)it.off + lane) * G + 4 * c0;
-            live = 0;
 #pragma unroll
-            for (int r = 0; r < R; r++) live |= (lane + 32 * r < it.ntok ? 1u : 0u) << r;
+            for (int r = 0; r < R; r++)
+                base[r] = a.scales + ((size_t)it.off + min(lane + 32 * r, it.ntok - 1)) * G + 4 * c0;
         };
         auto use = [&](int n, int, int, const uint32_t (&w)[R][kGroup]) {
             const int gs = n % SG;
@@ -476,18 +489,19 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             mbar_arrive(gfull0 + 8 * gs);
             return true;
         };
-        const int wide = (reinterpret_cast<uintptr_t>(a.scales) | (uintptr_t)G | (uintptr_t)(4 * c0)) & 15;
-        scale_groups<R, NT == 256 ? 1 : 3>(n_items, kcs, wide == 0 ? 16 : wide == 8 ? 8 : 4, (size_t)32 * G, begin, use);
-    } else if (warp == 2) {
+        scale_groups<R>(n_items, kcs, (uint32_t)reinterpret_cast<uintptr_t>(a.scales) | G | 4 * c0,
+                                                           begin, use);
+    } else if (warp == 2 || warp == kIssuer1) {
         // ------------------------------------------------ MMA issuer --
         const bool leader = elect_one();
-        Slot<SA> sl;
+        const int who = ISS == 1 ? 0 : __shfl_sync(0xffffffffu, warp == 2 ? 0 : 1, 0);
+        Slot<SA> sl;                                   // the group's first stage
         Slot<SG> sg;
         Slot<NBUF> sb;
         // `alive` turns false when a wait gave up.  The loops run on to their
         // ends all the same (doing nothing): an exit on a loaded value would
         // take every address in them out of the uniform registers.
-        bool alive = true, ready = false;              // ready: the next stage's tiles have landed
+        bool alive = true, ready = false;              // ready (one issuer): the next stage's tiles have landed
         const uint32_t tile_hi = (uint32_t)(umma_desc_sw128(0) >> 32), tile_lo = (uint32_t)umma_desc_sw128(0);
         const uint32_t atom_hi = (uint32_t)(desc_atom(0, 128) >> 32), atom_lo = (uint32_t)desc_atom(0, 128);
         auto atom = [&](uint32_t addr16) { return (uint64_t)atom_hi << 32 | (atom_lo + addr16); };
@@ -503,18 +517,25 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 if (in_seg == 0) alive = alive && mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1);
                 alive = alive && mbar_wait(gfull0 + 8 * sg.i, sg.ph);
                 const bool last = c + kGroup >= kcs, seg_end = last || in_seg + 1 == seg;
-                const uint32_t d = tmem + sb.i * NT;
+                const uint32_t d = tmem + (sb.i * ISS + who) * NT;
                 const uint32_t sf = tmem + Sh::SF_COL + sg.i * (kGroup * Sh::SF_STEP);
                 const uint32_t src = (sgroups + sg.i * Sh::GROUP) >> 4;
 #pragma unroll
-                for (int j = 0; j < kGroup; j += KS)
+                for (int jj = 0; jj < kGroup / KS / ISS; jj++) {
+                    const int j = (jj * ISS + who) * KS;               // first tile of this warp's stage
                     if (c + j < kcs) {
-                        alive = alive && (ready || mbar_wait(tfull0 + 8 * sl.i, sl.ph));
-                        const uint32_t slot = sl.i, wt = (ring + slot * Sh::STAGE) >> 4;
-                        sl.next();
-                        ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
+                        uint32_t slot = sl.i + jj * ISS + who, ph = sl.ph;
+                        if (slot >= SA) {
+                            slot -= SA;
+                            ph ^= 1;
+                        }
+                        alive = alive && ((ISS == 1 && ready) || mbar_wait(tfull0 + 8 * slot, ph));
+                        if (ISS == 1) {
+                            const bool wrap = slot + 1 == SA;
+                            ready = mbar_test(tfull0 + 8 * (wrap ? 0 : slot + 1), wrap ? ph ^ 1 : ph);
+                        }
+                        const uint32_t wt = (ring + slot * Sh::STAGE) >> 4;
                         tc_fence_after();
-                        const bool group_end = j + KS >= kGroup || c + j + KS >= kcs;
                         if (leader && alive) {
 #pragma unroll
                             for (int t = 0; t < KS; t++)
@@ -528,14 +549,19 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
                                     for (int ks = 0; ks < 4; ks++)
                                         mma_mxf8f6f4(d, desc(ad + 2 * ks), desc(bd + 2 * ks), id[ks], sfa, sfb,
-                                                     (in_seg | j | t | ks) != 0 ? 1u : 0u);
+                                                     (in_seg | jj | t | ks) != 0 ? 1u : 0u);
                                 }
                             umma_commit(empty0 + 8 * slot);
-                            if (group_end) umma_commit(gempty0 + 8 * sg.i);
-                            if (group_end && seg_end) umma_commit(accf0 + 8 * sb.i);
                         }
                         __syncwarp();
                     }
+                }
+                if (leader && alive) {
+                    umma_commit(gempty0 + 8 * sg.i);
+                    if (seg_end) umma_commit(accf0 + 8 * sb.i);
+                }
+                __syncwarp();
+                sl.add(min(kGroup / KS, (kcs - c + KS - 1) / KS));
                 sg.next();
                 in_seg++;
                 if (seg_end) {
@@ -570,23 +596,30 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
+            for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * ISS * NT + n0 + j, v + j);
             tmem_ld_wait();
+            // stages an accumulation holds: one stage is issuer 0's alone
+            const int seg_stages = seg * (kGroup / KS);
+            auto add = [&](uint32_t acc) {
+#pragma unroll
+                for (int j = 0; j < HC; j += 16)
+                    if (n0 + j < n1) {
+                        float u[16];
+                        tmem_ld16f(tmem + quarter + acc * NT + n0 + j, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) v[j + i] += u[i];
+                    }
+            };
+            if (ISS == 2 && min(seg_stages, fts) > 1) add(sb.i * ISS + 1);
             tc_fence_before();
             mbar_arrive(acce0 + 8 * sb.i);
             sb.next();
             for (int sg = 1; sg < n_seg; sg++, sb.next()) {
                 alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
                 tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < HC; j += 16)
-                    if (n0 + j < n1) {
-                        float u[16];
-                        tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; i++) v[j + i] += u[i];
-                    }
+                add(sb.i * ISS);
+                if (ISS == 2 && fts - sg * seg_stages > 1) add(sb.i * ISS + 1);
                 tc_fence_before();
                 mbar_arrive(acce0 + 8 * sb.i);
             }
@@ -717,7 +750,7 @@ cudaError_t launch_t(const Ctx &c, const ProdArgs &a, int y_bf16, int S, int clu
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(clusters * S));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Shape<NT>::THREADS);
     cfg.dynamicSmemBytes = Shape<NT>::SMEM;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];
@@ -745,7 +778,7 @@ int resident_clusters(const Ctx &c, int S) {
         static std::atomic<uint64_t> configured{0};
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(c.num_sms / S * S));
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(Shape<32>::THREADS);
         cfg.dynamicSmemBytes = Shape<32>::SMEM;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -783,9 +816,10 @@ Plan choose(const Ctx &c, const ProdArgs &a, int y_bf16) {
             long long clusters = resident_clusters(c, S);
             if (clusters > items) clusters = items;
             const long long waves = (items + clusters - 1) / clusters;
-            const int n = mean < NT ? (mean + 15) & ~15 : NT;
-            const double mma = 2.0 * (n < 64 ? 64 : n) + 60, mem = 8192.0 / (3400.0 / (double)(clusters * S) < 60 ? 3400.0 / (double)(clusters * S) : 60);
-            const double t = (double)waves * (((KC + S - 1) / S) * (mma > mem ? mma : mem) + 1000.0 + (S > 1 ? 500 : 0));
+            // us, fitted to a sweep of 24 shapes (rows 1-4096, out 1000-12288, in 1024-7168)
+            const int n = mean < NT ? mean : NT, tiles = ((KC + KS - 1) / KS + S - 1) / S * KS;
+            const double tile = NT == 32 ? 0.23 : NT == 64 ? 0.26 : NT == 128 ? 0.32 : 0.39;
+            const double t = (double)waves * (tiles * tile + (S == 1 ? 0.5 + 0.006 * n : 2.0 + 0.05 * n));
             if (best.NT == 0 || t < least) {
                 least = t;
                 best = Plan{NT, S, (int)clusters};
