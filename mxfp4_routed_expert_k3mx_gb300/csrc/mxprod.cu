@@ -594,6 +594,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             // for once.
             float v[HC];
             alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
+            __syncwarp();                       // (each lane polls for itself; the loads are the whole warp's)
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * ISS * NT + n0 + j, v + j);
@@ -617,6 +618,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             sb.next();
             for (int sg = 1; sg < n_seg; sg++, sb.next()) {
                 alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
+                __syncwarp();
                 tc_fence_after();
                 add(sb.i * ISS);
                 if (ISS == 2 && fts - sg * seg_stages > 1) add(sb.i * ISS + 1);
@@ -651,6 +653,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     if (x * kExCols >= it.ntok) break;
                     const int cols = (min(kExCols, it.ntok - x * kExCols) + 3) & ~3;
                     const uint32_t buf = smem_addr(red) + ex.i * kExBytes, bar = exfull0 + 8 * ex.i;
+                    __syncwarp();
                     named_sync(1, kEpiThreads);
                     if (warp == kEpi0 && lane == 0) mbar_arrive_expect_tx(bar, S * RS * cols * 16 / 4);
                     const uint32_t to = map_rank(buf + (rank * RS + o - own * RS) * (kExPitch * 4), own), tobar = map_rank(bar, own);
@@ -664,6 +667,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                         }
                     }
                     alive = alive && wait_cluster(bar, ex.ph);
+                    __syncwarp();
                     const float *src = reinterpret_cast<const float *>(red + ex.i * kExBytes);
                     for (int i = tid - kEpi0 * 32; i < RS * (cols / 4); i += kEpiThreads) {
                         const int n = i / RS * 4, r = i % RS, out = it.mt * 128 + rank * RS + r;
@@ -703,6 +707,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     if (warp == 2) {
         // no MMA may still be running when TMEM is released
         if (!mbar_wait_drain(done, 0) && lane == 0) report_status(a.status, kStatusWaitTimeout, 450);
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
