@@ -43,7 +43,7 @@ constexpr int kStageCols = 128;
 constexpr int kWTile = 128 * 128;          // weight tile in shared memory (spread codes)
 constexpr int kWTileTx = 128 * 64;         // bytes its copy moves
 constexpr int kAtom = 512;                 // scales of 128 rows and a tile: 32 lines of 16 bytes
-constexpr int kEpi0 = 4, kEpiThreads = 8 * 32, kIssuer1 = 12;   // warps; see the head of this file
+constexpr int kThreads = 12 * 32, kEpi0 = 4, kEpiThreads = 8 * 32;
 
 constexpr int kMaxSplit = 8;               // CTAs of a cluster: 1, 2, 4 or 8
 
@@ -65,19 +65,14 @@ template <int NT_> struct Shape {
     static constexpr int SA = NT == 64 ? 3 : NT == 128 ? 6 : 4;      // stages
     static constexpr int SG = 3;                                     // scale groups
     static constexpr int GROUP = kGroup * (1 + ATOMS) * kAtom;       // weights' atoms, then the rows'
-    // Warps that issue MMAs, the stages of an item dealt among them, each with
-    // accumulators of its own (the epilogue adds them): one's waits and
-    // address work overlap the other's MMAs.
-    static constexpr int ISS = NT <= 64 ? 2 : 1;
-    static constexpr int THREADS = ISS == 2 ? 13 * 32 : 12 * 32;
-    static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators of an issuer
+    static constexpr int NBUF = NT == 256 ? 1 : 2;                   // accumulators
     static constexpr bool SPLIT = NT <= 64;                          // clusters of more than one CTA
     static constexpr int RED = SPLIT ? 2 * kExBytes : 0;
     static constexpr int TABLES = 2 * (K3MX_MX_MAX_GROUPS + 8) * 4;
     static constexpr int SMEM = 1024 + 1024 + SA * STAGE + SG * GROUP + RED + TABLES;
     // TMEM columns: accumulators, then every tile's scales (addresses the MMA
     // reads scales from are multiples of four columns)
-    static constexpr int SF_COL = ISS * NBUF * NT, SF_STEP = 4 + 4 * ATOMS;
+    static constexpr int SF_COL = NBUF * NT, SF_STEP = 4 + 4 * ATOMS;
     static constexpr int TMEM_COLS = 512;
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
@@ -145,10 +140,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
     return p != 0;
 }
-__device__ __forceinline__ void tma_prefetch_3d(const void *map, int x, int y, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
@@ -172,9 +163,6 @@ template <int N> struct Slot {
             i = 0;
             ph ^= 1;
         }
-    }
-    __device__ __forceinline__ void add(uint32_t n) {          // n <= 2 N
-        for (i += n; i >= N; i -= N) ph ^= 1;
     }
 };
 
@@ -246,10 +234,10 @@ __device__ __forceinline__ void scale_groups(int n_items, int kcs, uint32_t bits
 }
 
 template <int NT>
-__global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, const __grid_constant__ Maps maps) {
     using Sh = Shape<NT>;
-    constexpr int SA = Sh::SA, SG = Sh::SG, NBUF = Sh::NBUF, KS = Sh::KS, ISS = Sh::ISS;
+    constexpr int SA = Sh::SA, SG = Sh::SG, NBUF = Sh::NBUF, KS = Sh::KS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Hdr *hd = reinterpret_cast<Hdr *>(smem);
@@ -272,13 +260,13 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         }
         for (int i = 0; i < SG; i++) {
             mbar_init(gfull0 + 8 * i, 64);
-            mbar_init(gempty0 + 8 * i, ISS);
+            mbar_init(gempty0 + 8 * i, 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(accf0 + 8 * i, ISS);
+            mbar_init(accf0 + 8 * i, 1);
             mbar_init(acce0 + 8 * i, kEpiThreads);
         }
-        mbar_init(done, ISS);
+        mbar_init(done, 1);
         mbar_init(exfull0, 1);
         mbar_init(exfull0 + 8, 1);
         hd->abort = 0;
@@ -292,7 +280,6 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     const int KF = (KC + KS - 1) / KS, f0 = KF * rank / S, f1 = KF * (rank + 1) / S;
     const int c0 = f0 * KS, kcs = min(f1 * KS, KC) - c0, fts = f1 - f0;
     const int first = blockIdx.x / S, step = gridDim.x / S;
-    pdl_launch_dependents();
     if (a.offsets == nullptr) {
         // One group of all rows: everything up to the copies is ready before
         // the kernel before this one ends, and the first weights are on their
@@ -302,26 +289,24 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             ustart[1] = (a.n_rows + NT - 1) / NT;
             goff[1] = a.n_rows;
         }
-        const int mt = first / ((a.n_rows + NT - 1) / NT);
-        if (mt < MT) {
-            if (warp == 0 && lane < SA && lane * KS < kcs)
-                tma_prefetch_3d(&maps.w, 0, mt * 128, c0 + lane * KS);
-            if (warp == 1)
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    if (mt * 128 + lane + 32 * r < a.out)
-                        prefetch_l2(a.wscales + (size_t)(mt * 128 + lane + 32 * r) * G + 4 * c0);
+        const int mt = first / ((a.n_rows + NT - 1) / NT), row = mt * 128 + (tid & 127);
+        if (row < a.out) {
+            // the first SA stages' codes (64 bytes a tile) and their scales
+            const uint8_t *w = a.packed + (size_t)row * (a.in / 2);
+            const int t = (tid >> 7) * 2;                             // three lines of 128 bytes
+            if (t < min(kcs, SA * KS)) prefetch_l2(w + (size_t)(c0 + t) * (kStageCols / 2));
+            if (tid < 128) prefetch_l2(a.wscales + (size_t)row * G + 4 * c0);
         }
     } else {
         pdl_wait();
         // units of every group (0 for one whose offsets are unusable)
-        constexpr int GPT = (K3MX_MX_MAX_GROUPS + 383) / 384;        // groups a thread (12 warps)
+        constexpr int GPT = (K3MX_MX_MAX_GROUPS + kThreads - 1) / kThreads;
         int nu[GPT], mine = 0;
 #pragma unroll
         for (int k = 0; k < GPT; k++) {
             const int g = tid * GPT + k;
             nu[k] = 0;
-            if (g < a.n_groups && tid < 384) {
+            if (g < a.n_groups) {
                 const int lo = __ldg(a.offsets + g), hi = __ldg(a.offsets + g + 1);
                 if (lo < 0 || hi < lo || hi > a.n_rows) {
                     if (blockIdx.x == 0) report_status(a.status, kStatusBadIndex, g);
@@ -348,7 +333,6 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
         for (int k = 0; k < GPT; k++) {
             const int g = tid * GPT + k;
-            if (tid >= 384) break;
             if (g < a.n_groups) ustart[g] = at;
             at += nu[k];
             if (g == a.n_groups - 1) ustart[a.n_groups] = at;
@@ -359,6 +343,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     else __syncthreads();
     tc_fence_after();
     if (a.offsets == nullptr) pdl_wait();
+    pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, hd->tmem, 0);
     volatile int *abort_flag = &hd->abort;
 
@@ -491,17 +476,16 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         };
         scale_groups<R>(n_items, kcs, (uint32_t)reinterpret_cast<uintptr_t>(a.scales) | G | 4 * c0,
                                                            begin, use);
-    } else if (warp == 2 || warp == kIssuer1) {
+    } else if (warp == 2) {
         // ------------------------------------------------ MMA issuer --
         const bool leader = elect_one();
-        const int who = ISS == 1 ? 0 : __shfl_sync(0xffffffffu, warp == 2 ? 0 : 1, 0);
-        Slot<SA> sl;                                   // the group's first stage
+        Slot<SA> sl;
         Slot<SG> sg;
         Slot<NBUF> sb;
         // `alive` turns false when a wait gave up.  The loops run on to their
         // ends all the same (doing nothing): an exit on a loaded value would
         // take every address in them out of the uniform registers.
-        bool alive = true, ready = false;              // ready (one issuer): the next stage's tiles have landed
+        bool alive = true, ready = false;              // ready: the next stage's tiles have landed
         const uint32_t tile_hi = (uint32_t)(umma_desc_sw128(0) >> 32), tile_lo = (uint32_t)umma_desc_sw128(0);
         const uint32_t atom_hi = (uint32_t)(desc_atom(0, 128) >> 32), atom_lo = (uint32_t)desc_atom(0, 128);
         auto atom = [&](uint32_t addr16) { return (uint64_t)atom_hi << 32 | (atom_lo + addr16); };
@@ -517,23 +501,16 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 if (in_seg == 0) alive = alive && mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1);
                 alive = alive && mbar_wait(gfull0 + 8 * sg.i, sg.ph);
                 const bool last = c + kGroup >= kcs, seg_end = last || in_seg + 1 == seg;
-                const uint32_t d = tmem + (sb.i * ISS + who) * NT;
+                const uint32_t d = tmem + sb.i * NT;
                 const uint32_t sf = tmem + Sh::SF_COL + sg.i * (kGroup * Sh::SF_STEP);
                 const uint32_t src = (sgroups + sg.i * Sh::GROUP) >> 4;
 #pragma unroll
-                for (int jj = 0; jj < kGroup / KS / ISS; jj++) {
-                    const int j = (jj * ISS + who) * KS;               // first tile of this warp's stage
+                for (int j = 0; j < kGroup; j += KS) {
                     if (c + j < kcs) {
-                        uint32_t slot = sl.i + jj * ISS + who, ph = sl.ph;
-                        if (slot >= SA) {
-                            slot -= SA;
-                            ph ^= 1;
-                        }
-                        alive = alive && ((ISS == 1 && ready) || mbar_wait(tfull0 + 8 * slot, ph));
-                        if (ISS == 1) {
-                            const bool wrap = slot + 1 == SA;
-                            ready = mbar_test(tfull0 + 8 * (wrap ? 0 : slot + 1), wrap ? ph ^ 1 : ph);
-                        }
+                        alive = alive && (ready || mbar_wait(tfull0 + 8 * sl.i, sl.ph));
+                        const uint32_t slot = sl.i;
+                        sl.next();
+                        ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
                         const uint32_t wt = (ring + slot * Sh::STAGE) >> 4;
                         tc_fence_after();
                         if (leader && alive) {
@@ -549,7 +526,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
                                     for (int ks = 0; ks < 4; ks++)
                                         mma_mxf8f6f4(d, desc(ad + 2 * ks), desc(bd + 2 * ks), id[ks], sfa, sfb,
-                                                     (in_seg | jj | t | ks) != 0 ? 1u : 0u);
+                                                     (in_seg | j | t | ks) != 0 ? 1u : 0u);
                                 }
                             umma_commit(empty0 + 8 * slot);
                         }
@@ -561,7 +538,6 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     if (seg_end) umma_commit(accf0 + 8 * sb.i);
                 }
                 __syncwarp();
-                sl.add(min(kGroup / KS, (kcs - c + KS - 1) / KS));
                 sg.next();
                 in_seg++;
                 if (seg_end) {
@@ -597,22 +573,8 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             __syncwarp();                       // (each lane polls for itself; the loads are the whole warp's)
             tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * ISS * NT + n0 + j, v + j);
+            for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
             tmem_ld_wait();
-            // stages an accumulation holds: one stage is issuer 0's alone
-            const int seg_stages = seg * (kGroup / KS);
-            auto add = [&](uint32_t acc) {
-#pragma unroll
-                for (int j = 0; j < HC; j += 16)
-                    if (n0 + j < n1) {
-                        float u[16];
-                        tmem_ld16f(tmem + quarter + acc * NT + n0 + j, u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; i++) v[j + i] += u[i];
-                    }
-            };
-            if (ISS == 2 && min(seg_stages, fts) > 1) add(sb.i * ISS + 1);
             tc_fence_before();
             mbar_arrive(acce0 + 8 * sb.i);
             sb.next();
@@ -620,8 +582,15 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
                 __syncwarp();
                 tc_fence_after();
-                add(sb.i * ISS);
-                if (ISS == 2 && fts - sg * seg_stages > 1) add(sb.i * ISS + 1);
+#pragma unroll
+                for (int j = 0; j < HC; j += 16)
+                    if (n0 + j < n1) {
+                        float u[16];
+                        tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) v[j + i] += u[i];
+                    }
                 tc_fence_before();
                 mbar_arrive(acce0 + 8 * sb.i);
             }
@@ -755,7 +724,7 @@ cudaError_t launch_t(const Ctx &c, const ProdArgs &a, int y_bf16, int S, int clu
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(clusters * S));
-    cfg.blockDim = dim3(Shape<NT>::THREADS);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Shape<NT>::SMEM;
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];
@@ -783,7 +752,7 @@ int resident_clusters(const Ctx &c, int S) {
         static std::atomic<uint64_t> configured{0};
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(c.num_sms / S * S));
-        cfg.blockDim = dim3(Shape<32>::THREADS);
+        cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = Shape<32>::SMEM;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
