@@ -480,6 +480,9 @@ def _mx_refuse(rows, cols, fmt, shapes, bytes_=(), values=(), strided=None):
 
 def _mx_rows(x, name):
     """(rows, cols, pitch) of a 2-D tensor of contiguous rows."""
+    if isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_contiguous():
+        rows, cols = x.shape
+        return rows, cols, cols
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise TypeError(f"{name}: 2-D tensor of contiguous rows expected (shape [rows, cols], column stride 1)")
     rows, cols = x.shape
@@ -568,7 +571,7 @@ def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
     rows, inner, _ = _mx_rows(codes, "codes")
     out, dt = (y.shape[-1] if y.dim() else 0), _MX_DTYPES.get(y.dtype)
     if not (dt is not None and y.shape == (rows, out) and y.is_cuda and y.is_contiguous() and inner % 32 == 0 and
-            _mx_bytes(codes, (rows, inner)) and _mx_bytes(scales, (rows, inner // 32)) and
+            codes.dtype is _U8 and codes.is_cuda and codes.is_contiguous() and _mx_bytes(scales, (rows, inner // 32)) and
             _mx_bytes(packed, (out, inner // 2)) and _mx_bytes(wscales, (out, inner // 32))):
         _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, ())
     _check("k3mx_mx_linear", (_lib or lib()).k3mx_mx_linear(

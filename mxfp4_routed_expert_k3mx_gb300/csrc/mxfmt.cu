@@ -150,48 +150,36 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], uint8_t *codes, uint8
 // U runs of eight values a lane, a CTA's threads apart: U loads in flight.
 constexpr int kFmtThreads = 256;
 
-// x rows ldx apart, `per_row` = cols / 8 runs to a row; FLAT: ldx = cols, so
-// that a run's place needs no division.
+// FLAT: ldx = cols, the matrix is one line of n8 runs.  Else the grid's y
+// walks the rows and its x a row's per_row = cols / 8 runs, so that a run's
+// place takes no division (35 us a call with one, 26 without, for 4096 rows of
+// 7168 bf16 to MXFP8 and back).
 template <int FMT, bool BF16, bool VEC, bool FLAT, int U>
 __global__ void __launch_bounds__(kFmtThreads)
-k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int per_row, int64_t ldx, int *status) {
+k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int per_row, int64_t ldx, int rows, int *status) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t i0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;
-    // the CTA's first run: one division a CTA
-    const int64_t row0 = FLAT ? 0 : (i0 - threadIdx.x) / per_row;
-    const int col0 = FLAT ? 0 : (int)(i0 - threadIdx.x - row0 * per_row);
-    float v[U][8];
+    const int64_t c0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;
+    int row = FLAT ? 0 : blockIdx.y;
+    do {
+        const int64_t from = FLAT ? 0 : row * ldx, to = FLAT ? 0 : (int64_t)row * per_row;
+        float v[U][8];
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int64_t i = i0 + u * kFmtThreads;       // whole blocks: n8 is a multiple of 4
+        for (int u = 0; u < U; u++) {
+            const int64_t c = c0 + u * kFmtThreads;       // whole blocks: the line is a multiple of 4 runs
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[u][j] = 0.f;
-        if (i < n8) {
-            int64_t at = 8 * i;
-            if (!FLAT) {
-                int64_t r = row0;
-                int c = col0 + (int)threadIdx.x + u * kFmtThreads;
-                if (per_row >= kFmtThreads) {          // at most U rows on
-                    while (c >= per_row) {
-                        c -= per_row;
-                        r++;
-                    }
-                } else {
-                    r += c / per_row;
-                    c %= per_row;
-                }
-                at = r * ldx + c * 8;
-            }
-            load8<BF16, VEC>(x, at, v[u]);
+            for (int j = 0; j < 8; j++) v[u][j] = 0.f;
+            if (c < n8) load8<BF16, VEC>(x, from + 8 * c, v[u]);
         }
-    }
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int64_t i = i0 + u * kFmtThreads;
-        const uint32_t s = encode8<FMT>(v[u], codes, scales, i, i < n8);
-        if (FMT == K3MX_MXFP4 && s == 255u && i < n8) report_status(status, kStatusBadIndex, (int)(i / per_row));
-    }
+        for (int u = 0; u < U; u++) {
+            const int64_t c = c0 + u * kFmtThreads;
+            const uint32_t s = encode8<FMT>(v[u], codes, scales, to + c, c < n8);
+            if (FMT == K3MX_MXFP4 && s == 255u && c < n8)
+                report_status(status, kStatusBadIndex, FLAT ? (int)(c / per_row) : row);
+        }
+        row += gridDim.y;
+    } while (!FLAT && row < rows);
 }
 
 template <int FMT, bool BF16, int U>
@@ -294,7 +282,14 @@ __global__ void __launch_bounds__(WARP ? 128 : V == 1 ? 1024 : V == 2 ? 512 : 10
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    const float k = 1.0f / sqrtf(ss / (float)a.width + a.eps);
+    // 1 / sqrt(mean + eps) as k + kl, and below g times that as gk + gl, so that
+    // a value is rounded once: one near the middle of two codes then goes the
+    // way the exact one does unless it is within about 2^-24 of it.
+    const float w = (float)a.width, q = ss / w, m = q + a.eps;
+    const float ml = ((q - m) + a.eps) + fmaf(-q, w, ss) / w;         // what q and m were rounded by
+    const float k = rsqrtf(m), k2 = k * k;
+    float kl = 0.5f * k * (fmaf(-m, k2, 1.0f) - m * fmaf(k, k, -k2) - ml * k2);
+    if (!(m > 0.f && m < INFINITY)) kl = 0.f;
 #pragma unroll
     for (int p = 0; p < V; p++) {
         const int i = p * P + i0;
@@ -303,7 +298,10 @@ __global__ void __launch_bounds__(WARP ? 128 : V == 1 ? 1024 : V == 2 ? 512 : 10
             float g[8];
             load8<true, true>(a.g, 8 * i, g);
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[p][j] = v[p][j] * k * g[j];
+            for (int j = 0; j < 8; j++) {
+                const float gk = g[j] * k, gl = fmaf(g[j], kl, fmaf(g[j], k, -gk));
+                v[p][j] = fmaf(v[p][j], gk, v[p][j] * gl);
+            }
             if (a.normed != nullptr) store8<true>(a.normed, t * a.width + 8 * i, v[p], true);
         }
         encode8<K3MX_MXFP8>(v[p], a.codes, a.scales, t * per_row + i, live);
@@ -321,7 +319,6 @@ cudaError_t norm_t(const Ctx &c, const NormArgs &a, int bf16) {
 }  // namespace
 
 // Runs a lane: four where that still fills the device several times over.
-// (4096 x 7168 bf16 to MXFP8 and back, us: see the table of measurements.)
 static bool many_runs(const Ctx &c, int64_t n8) { return n8 >= (int64_t)c.num_sms * 8 * kFmtThreads * 4; }
 
 template <int FMT, bool BF16>
@@ -329,15 +326,17 @@ static cudaError_t quantize_t(const Ctx &c, uint8_t *codes, uint8_t *scales, con
                               int64_t ldx) {
     const int64_t n8 = (int64_t)rows * cols / 8;
     const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * (BF16 ? 2 : 4)) % 16 == 0;
-    auto go = [&](auto kernel, int U) {
-        const dim3 grid((unsigned)((n8 + kFmtThreads * U - 1) / (kFmtThreads * U)));
-        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, codes, scales, x, n8, cols / 8, ldx, c.status);
+    // a line of `n` runs, `lines` of them
+    auto go = [&](auto kernel, int U, int64_t n, int lines) {
+        const dim3 grid((unsigned)((n + kFmtThreads * U - 1) / (kFmtThreads * U)), (unsigned)(lines < 65535 ? lines : 65535));
+        return launch_pdl(kernel, grid, dim3(kFmtThreads), 0, c.stream, codes, scales, x, n, cols / 8, ldx, lines, c.status);
     };
-    if (!vec) return go(k_mx_quantize<FMT, BF16, false, false, 1>, 1);
-    if (ldx != cols) return many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, false, 4>, 4)
-                                             : go(k_mx_quantize<FMT, BF16, true, false, 1>, 1);
-    return many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, true, 4>, 4)
-                            : go(k_mx_quantize<FMT, BF16, true, true, 1>, 1);
+    if (!vec) return go(k_mx_quantize<FMT, BF16, false, false, 1>, 1, cols / 8, rows);
+    if (ldx != cols)
+        return cols / 8 > kFmtThreads && many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, false, 4>, 4, cols / 8, rows)
+                                                          : go(k_mx_quantize<FMT, BF16, true, false, 1>, 1, cols / 8, rows);
+    return many_runs(c, n8) ? go(k_mx_quantize<FMT, BF16, true, true, 4>, 4, n8, 1)
+                            : go(k_mx_quantize<FMT, BF16, true, true, 1>, 1, n8, 1);
 }
 
 cudaError_t launch_mx_quantize(const Ctx &c, uint8_t *codes, uint8_t *scales, const void *x, int x_bf16, int rows,
