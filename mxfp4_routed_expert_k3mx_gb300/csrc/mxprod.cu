@@ -665,11 +665,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             }
             if (*abort_flag) alive = false;
         }
-        if (!alive) {
-            if (lane == 0) fail(440);
-            // parts of others may still be under way to this CTA
-            for (int i = 0; S > 1 && i < 100; i++) __nanosleep(1000);
-        }
+        if (!alive && lane == 0) fail(440);
     }
 
     __syncthreads();
@@ -680,7 +676,12 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         tc_fence_after();
         tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
-    if (S > 1) cluster_sync();               // no CTA leaves while another may write to its shared memory
+    if (S > 1) {
+        cluster_sync();                      // no CTA leaves while another may write to its shared memory
+        // a CTA that gave up waiting has not seen all parts land; all are sent by now
+        if (tid == 0 && *abort_flag)
+            for (int i = 0; i < 100; i++) __nanosleep(1000);
+    }
 }
 
 // ------------------------------------------------------------- launchers --

@@ -198,3 +198,27 @@ def test_norm_of_nan_row_is_nan_blocks(cuda_dev):
     ref = run_norm(x[ok].contiguous(), None, w, 1e-5)
     assert torch.equal(codes[ok], ref[0]) and torch.equal(scales[ok], ref[1])
     assert k3mx.k3mx_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_past_2_31_elements(cuda_dev, fmt):
+    """300 000 rows of 7200 bf16 (flat, then strided): the last rows lie past
+    2^32 bytes of x and 2^31 codes."""
+    rows, cols = 300_000, 7200
+    wide = torch.zeros(rows, cols + 8, dtype=BF16, device=cuda_dev)
+    pick = torch.tensor([0, 1, 149_130, 298_261, 298_262, rows - 1], device=cuda_dev)
+    wide[pick] = torch.randn(len(pick), cols + 8, device=cuda_dev).to(BF16)
+    for x in (wide[:, :cols], wide.view(-1)[:rows * cols].view(rows, cols)):
+        vals = x[pick].double().cpu().numpy()
+        codes = torch.empty(rows, cols // 2 if fmt == k3mx.K3MX_MXFP4 else cols, dtype=torch.uint8, device=cuda_dev)
+        scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device=cuda_dev)
+        k3mx.k3mx_mx_quantize(codes, scales, x, fmt)
+        got = codes[pick].cpu().numpy()
+        rc, rs = mx_ref.quantize(vals, fmt)
+        assert np.array_equal(mx_ref.unpack(got) if fmt == k3mx.K3MX_MXFP4 else got, rc)
+        assert np.array_equal(scales[pick].cpu().numpy(), rs)
+        y = torch.empty(rows, cols, dtype=BF16, device=cuda_dev)
+        k3mx.k3mx_mx_dequantize(y, codes, scales, fmt)
+        ref = torch.from_numpy(mx_ref.values(rc, rs, fmt)).to(BF16)
+        assert torch.equal(y[pick].cpu(), ref)
+        del codes, scales, y

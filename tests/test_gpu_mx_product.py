@@ -215,3 +215,113 @@ def test_norm_quantize_product_chain(cuda_dev):
     k3mx.k3mx_mx_linear(y, c, s, p, ws)
     ref, ad = mx_ref.product(*[v.cpu().numpy() for v in (c, s, p, ws)])
     assert_close(y, ref, ad, F32)
+
+
+def test_products_in_a_graph(cuda_dev):
+    """Captured once, replayed on changed inputs."""
+    a = inputs(40, 1024, (300,), 21)
+    d = dev(*a)
+    y = torch.empty(40, 300, device="cuda:0")
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        k3mx.k3mx_mx_linear(y, *d)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            k3mx.k3mx_mx_linear(y, *d)
+        b = inputs(40, 1024, (300,), 22)
+        for t, n in zip(d, dev(*b)):
+            t.copy_(n)
+        g.replay()
+        s.synchronize()
+    ref, ad = mx_ref.product(*b)
+    assert_close(y, ref, ad, F32)
+
+
+def test_product_reads_what_the_kernel_before_wrote(cuda_dev):
+    """Weights, activations and offsets written by the launches right before
+    the product on the stream, many times over with changing values."""
+    rng = np.random.default_rng(5)
+    t, inner, out = 3, 512, 256
+    w = [torch.from_numpy(rng.standard_normal((out, inner)).astype(np.float32)).to("cuda:0") for _ in range(2)]
+    x = [torch.from_numpy(rng.standard_normal((t, inner)).astype(np.float32)).to("cuda:0") for _ in range(2)]
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda:0")
+    ref = []
+    for i in range(2):
+        p, ws, c, s = u8(out, inner // 2), u8(out, inner // 32), u8(t, inner), u8(t, inner // 32)
+        k3mx.k3mx_mx_quantize(p, ws, w[i], k3mx.K3MX_MXFP4)
+        k3mx.k3mx_mx_quantize(c, s, x[i], k3mx.K3MX_MXFP8)
+        torch.cuda.synchronize()
+        y = torch.empty(t, out, device="cuda:0")
+        k3mx.k3mx_mx_linear(y, c, s, p, ws)
+        torch.cuda.synchronize()
+        ref.append(y)
+    ys = [torch.empty(t, out, device="cuda:0") for _ in range(200)]
+    for i, y in enumerate(ys):
+        k3mx.k3mx_mx_quantize(c, s, x[i % 2], k3mx.K3MX_MXFP8)
+        k3mx.k3mx_mx_quantize(p, ws, w[i % 2], k3mx.K3MX_MXFP4)
+        k3mx.k3mx_mx_linear(y, c, s, p, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref[i % 2]) for i, y in enumerate(ys))
+
+
+@pytest.mark.parametrize("rows,inner,out", [(2, 65536, 1000), (40, 65536, 1000), (100, 65536, 300), (300, 65536, 300)])
+def test_product_waits_are_bounded(cuda_dev, rows, inner, out):
+    """With a limit of one poll a wait gives up (the epilogue's, for bf16 sums
+    of 512 tiles in one accumulation, lasts many polls): the status says so,
+    nothing faults, and with the limit restored the next call is right."""
+    a = inputs(rows, inner, (out,), rows)
+    d = dev(*a)
+    clean = torch.empty(rows, out, dtype=BF16, device="cuda:0")
+    k3mx.k3mx_mx_linear(clean, *d)
+    assert k3mx.k3mx_device_status() == (0, 0)
+    y = torch.empty_like(clean)
+    k3mx.k3mx_set_wait_limit(1)
+    try:
+        seen = 0
+        for _ in range(50):
+            k3mx.k3mx_mx_linear(y, *d)
+            st, detail = k3mx.k3mx_device_status()
+            assert st in (0, 6), (st, detail)
+            if st == 6:
+                assert 400 <= detail < 460
+                seen += 1
+                break
+    finally:
+        k3mx.k3mx_set_wait_limit(0)
+    assert seen, "no wait ran out"
+    y.fill_(0)
+    k3mx.k3mx_mx_linear(y, *d)
+    assert k3mx.k3mx_device_status() == (0, 0)
+    assert torch.equal(y, clean)
+
+
+# ------------------------------------------------- offsets past 32 bits --
+
+def test_grouped_weights_past_4_gib(cuda_dev):
+    """Group 70 of 72 matrices of 64 MiB: its codes start past 2^32 bytes."""
+    E, out, inner, rows = 72, 8192, 16384, 5
+    packed = torch.zeros(E, out, inner // 2, dtype=torch.uint8, device="cuda:0")
+    wscales = torch.full((E, out, inner // 32), 120, dtype=torch.uint8, device="cuda:0")
+    gen = torch.Generator(device="cuda:0").manual_seed(0)
+    packed[70] = torch.randint(0, 256, (out, inner // 2), generator=gen, device="cuda:0", dtype=torch.uint8)
+    packed[69] = 0x11
+    xc, xs, _, _ = inputs(rows, inner, (1,), 3)
+    off = np.array([0] * 70 + [2, rows, rows], np.int32)          # group 69: rows 0-1, group 70: rows 2-4
+    y = torch.empty(rows, out, device="cuda:0")
+    k3mx.k3mx_mx_grouped(y, *dev(xc, xs), packed, wscales, torch.from_numpy(off).to("cuda:0"))
+    pick = np.array([0, 1, 127, 128, 5000, 8190, 8191])
+    for g, lo, hi in ((69, 0, 2), (70, 2, rows)):
+        ref, ad = mx_ref.product(xc[lo:hi], xs[lo:hi], packed[g, pick].cpu().numpy(), wscales[g, pick].cpu().numpy())
+        assert_close(y[lo:hi][:, pick], ref, ad, F32)
+
+
+def test_linear_output_past_4_gib(cuda_dev):
+    """y of 2^31 + elements: the last rows lie past 2^32 bytes."""
+    rows, inner, out = 70_000, 128, 32_768
+    xc, xs, p, ws = inputs(rows, inner, (out,), 9)
+    y = torch.empty(rows, out, dtype=BF16, device="cuda:0")
+    k3mx.k3mx_mx_linear(y, *dev(xc, xs, p, ws))
+    pick = np.array([0, 1, 255, 256, 40_000, 65_535, 65_536, 69_998, 69_999])
+    ref, ad = mx_ref.product(xc[pick], xs[pick], p, ws)
+    assert_close(y[torch.from_numpy(pick).to("cuda:0")], ref, ad, BF16)
