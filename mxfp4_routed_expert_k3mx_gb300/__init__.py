@@ -434,20 +434,22 @@ def k3mx_moe_routed_host(y_host, x_host, experts, logits_host, bias_host, worksp
 
 # ------------------------------------------------ microscaled operators --
 #
-# One-token calls last a few microseconds on the device, so each function
-# first asks in one expression whether its arguments are as they should be
-# (2 us for six tensors) and names what is wrong only when they are not.
+# One-token calls last a few microseconds on the device, and the host's share
+# of a call is of that size.  So each function asks in one expression, with
+# no call of its own, whether its arguments are as they should be, and only
+# where they are not looks for what is wrong and names it.
 
 _MX_DTYPES = {torch.float32: K3MX_F32, torch.bfloat16: K3MX_BF16}
-_U8 = torch.uint8
+_U8, _BF16 = torch.uint8, torch.bfloat16
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _mx_bytes(t, shape):
-    return t.dtype is _U8 and t.shape == shape and t.is_cuda and t.is_contiguous()
-
-
-def _mx_values(t, shape, dtype):
-    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+def _entry(name):
+    """A C function by name, put in this module's place for it at its first call."""
+    def first(*args):
+        func = globals()[name[len("k3mx"):]] = getattr(lib(), name)
+        return func(*args)
+    return first
 
 
 def _mx_need(t, shape, name):
@@ -456,7 +458,17 @@ def _mx_need(t, shape, name):
         raise TypeError(f"{name}: shape {list(shape)} expected, got {got}")
 
 
-def _mx_refuse(rows, cols, fmt, shapes, bytes_=(), values=(), strided=None):
+def _mx_rows(x, name):
+    """(rows, cols) of a 2-D tensor of contiguous rows."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise TypeError(f"{name}: 2-D tensor of contiguous rows expected (shape [rows, cols], column stride 1)")
+    rows, cols = x.shape
+    if rows > 1 and x.stride(0) < cols:
+        raise TypeError(f"{name}: rows overlap (shape {list(x.shape)}, row stride {x.stride(0)})")
+    return rows, cols
+
+
+def _mx_refuse(rows, cols, fmt, shapes, bytes_, values, strided=None):
     """Raises for the first argument that is not as expected: format and
     sizes, then shapes, then types and devices.  shapes: (tensor, shape, name);
     bytes_, values: (tensor, name), values of `strided`'s or their own type."""
@@ -466,7 +478,7 @@ def _mx_refuse(rows, cols, fmt, shapes, bytes_=(), values=(), strided=None):
         raise TypeError(f"at least one row and columns in blocks of 32 expected (shape), got {rows} x {cols}")
     for t, shape, name in shapes:
         _mx_need(t, shape, name)
-    for t, name in (([strided] if strided else []) + list(values)):
+    for t, name in (([strided] if strided else []) + values):
         if t.dtype not in _MX_DTYPES:
             raise TypeError(f"{name}: float32 or bfloat16 tensor expected")
     for t, name in bytes_:
@@ -475,51 +487,63 @@ def _mx_refuse(rows, cols, fmt, shapes, bytes_=(), values=(), strided=None):
         _dev(t, strided[0].dtype if strided else t.dtype, name)
     if strided and not strided[0].is_cuda:
         raise TypeError(f"{strided[1]}: CUDA tensor expected")
-    raise TypeError("arguments on different devices, or of unexpected layout")
+    raise TypeError("arguments of unexpected type, device or layout")
 
 
-def _mx_rows(x, name):
-    """(rows, cols, pitch) of a 2-D tensor of contiguous rows."""
-    if isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_contiguous():
-        rows, cols = x.shape
-        return rows, cols, cols
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise TypeError(f"{name}: 2-D tensor of contiguous rows expected (shape [rows, cols], column stride 1)")
-    rows, cols = x.shape
-    pitch = x.stride(0) if rows > 1 else cols
-    if pitch < cols:
-        raise TypeError(f"{name}: rows overlap (shape {list(x.shape)}, row stride {pitch})")
-    return rows, cols, pitch
+_mx_quantize = _entry("k3mx_mx_quantize")
+_mx_dequantize = _entry("k3mx_mx_dequantize")
+_rmsnorm_mx = _entry("k3mx_rmsnorm_mx")
+_mx_linear = _entry("k3mx_mx_linear")
+_mx_grouped = _entry("k3mx_mx_grouped")
 
 
 def k3mx_mx_quantize(codes, scales, x, fmt, stream=None):
     """x [rows, cols] (float32 or bfloat16, rows may be strided) to microscaled
     codes (uint8 [rows, cols/2] for K3MX_MXFP4, [rows, cols] for K3MX_MXFP8)
     and scale bytes (uint8 [rows, cols/32])."""
-    rows, cols, pitch = _mx_rows(x, "x")
-    wide = (rows, cols // 2 if fmt == K3MX_MXFP4 else cols)
-    dt = _MX_DTYPES.get(x.dtype)
-    if not (dt is not None and x.is_cuda and cols % 32 == 0 and _mx_bytes(codes, wide) and
-            _mx_bytes(scales, (rows, cols // 32))):
-        _mx_refuse(rows, cols, fmt, [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales")],
-                   [(codes, "codes"), (scales, "scales")], strided=(x, "x"))
-    _check("k3mx_mx_quantize", (_lib or lib()).k3mx_mx_quantize(
-        codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows, cols, pitch, fmt, _stream(stream)))
+    try:
+        rows, cols = x.shape
+        dt = _MX_DTYPES[x.dtype]
+        pitch = cols if x.is_contiguous() else x.stride(0) if x.stride(1) == 1 else -1
+        ok = (codes.shape == (rows, cols if fmt == 1 else cols // 2) and scales.shape == (rows, cols // 32) and
+              (fmt == 1 or fmt == 0) and cols % 32 == 0 and rows and (pitch >= cols or rows == 1 and pitch >= 0) and
+              codes.dtype is _U8 and scales.dtype is _U8 and x.is_cuda and codes.is_cuda and scales.is_cuda and
+              codes.is_contiguous() and scales.is_contiguous())
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        rows, cols = _mx_rows(x, "x")
+        _mx_refuse(rows, cols, fmt, [(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), "codes"),
+                                     (scales, (rows, cols // 32), "scales")],
+                   [(codes, "codes"), (scales, "scales")], [], strided=(x, "x"))
+    st = _mx_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows, cols, pitch if rows > 1 else cols, fmt,
+                      _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        _check("k3mx_mx_quantize", st)
     return codes, scales
 
 
 def k3mx_mx_dequantize(y, codes, scales, fmt, stream=None):
     """The values that codes and scale bytes stand for, in y [rows, cols]
     (float32: exact; bfloat16: rounded to nearest)."""
-    rows, cols, _ = _mx_rows(y, "y")
-    wide = (rows, cols // 2 if fmt == K3MX_MXFP4 else cols)
-    dt = _MX_DTYPES.get(y.dtype)
-    if not (dt is not None and y.is_cuda and y.is_contiguous() and cols % 32 == 0 and _mx_bytes(codes, wide) and
-            _mx_bytes(scales, (rows, cols // 32))):
-        _mx_refuse(rows, cols, fmt, [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales")],
+    try:
+        rows, cols = y.shape
+        dt = _MX_DTYPES[y.dtype]
+        ok = (codes.shape == (rows, cols if fmt == 1 else cols // 2) and scales.shape == (rows, cols // 32) and
+              (fmt == 1 or fmt == 0) and cols % 32 == 0 and rows and codes.dtype is _U8 and scales.dtype is _U8 and
+              y.is_cuda and codes.is_cuda and scales.is_cuda and
+              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous())
+    except (AttributeError, KeyError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        rows, cols = _mx_rows(y, "y")
+        _mx_refuse(rows, cols, fmt, [(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), "codes"),
+                                     (scales, (rows, cols // 32), "scales")],
                    [(codes, "codes"), (scales, "scales")], [(y, "y")])
-    _check("k3mx_mx_dequantize", (_lib or lib()).k3mx_mx_dequantize(
-        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows, cols, fmt, _stream(stream)))
+    st = _mx_dequantize(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows, cols, fmt,
+                        _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        _check("k3mx_mx_dequantize", st)
     return y
 
 
@@ -529,33 +553,46 @@ def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, s
     float32 or bfloat16 (rows may be strided), residual and sum of the same
     type (both None: no residual; sum may be residual itself), weight
     bfloat16 [width]."""
-    rows, cols, pitch = _mx_rows(x, "x")
-    if (residual is None) != (sum is None):
-        raise TypeError("sum: expected exactly where residual is given (shape of x)")
-    wide, dt = (rows, cols), _MX_DTYPES.get(x.dtype)
-    if not (dt is not None and x.is_cuda and cols % 32 == 0 and _mx_bytes(codes, wide) and
-            _mx_bytes(scales, (rows, cols // 32)) and _mx_values(weight, (cols,), torch.bfloat16) and
-            (residual is None or (_mx_values(residual, wide, x.dtype) and _mx_values(sum, wide, x.dtype))) and
-            (normed is None or _mx_values(normed, wide, torch.bfloat16))):
+    try:
+        wide = rows, cols = tuple(x.shape)
+        dt, kind = _MX_DTYPES[x.dtype], x.dtype
+        pitch = cols if x.is_contiguous() else x.stride(0) if x.stride(1) == 1 else -1
+        ok = (codes.shape == wide and scales.shape == (rows, cols // 32) and weight.shape == (cols,) and
+              cols % 32 == 0 and rows and (pitch >= cols or rows == 1 and pitch >= 0) and
+              codes.dtype is _U8 and scales.dtype is _U8 and weight.dtype is _BF16 and
+              x.is_cuda and codes.is_cuda and scales.is_cuda and weight.is_cuda and
+              codes.is_contiguous() and scales.is_contiguous() and weight.is_contiguous() and
+              (residual is None and sum is None or
+               residual.shape == wide and sum.shape == wide and residual.dtype is kind and sum.dtype is kind and
+               residual.is_cuda and sum.is_cuda and residual.is_contiguous() and sum.is_contiguous()) and
+              (normed is None or normed.shape == wide and normed.dtype is _BF16 and normed.is_cuda and
+               normed.is_contiguous()))
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        rows, cols = _mx_rows(x, "x")
+        if (residual is None) != (sum is None):
+            raise TypeError("sum: expected exactly where residual is given (shape of x)")
         given = [(t, n) for t, n in ((residual, "residual"), (sum, "sum")) if t is not None]
-        shapes = [(codes, wide, "codes"), (scales, (rows, cols // 32), "scales"), (weight, (cols,), "weight")]
-        if normed is not None:
-            shapes.append((normed, wide, "normed"))
-        for t, shape, n in shapes + [(t, wide, n) for t, n in given]:
+        shapes = [(codes, (rows, cols), "codes"), (scales, (rows, cols // 32), "scales"), (weight, (cols,), "weight")]
+        for t, shape, n in (shapes + [(t, (rows, cols), n) for t, n in given] +
+                            ([(normed, (rows, cols), "normed")] if normed is not None else [])):
             _mx_need(t, shape, n)
-        _dev(weight, torch.bfloat16, "weight")
-        _dev_opt(normed, torch.bfloat16, "normed")
+        _dev(weight, _BF16, "weight")
+        _dev_opt(normed, _BF16, "normed")
         _mx_refuse(rows, cols, K3MX_MXFP8, [], [(codes, "codes"), (scales, "scales")], given, strided=(x, "x"))
-    _check("k3mx_rmsnorm_mx", (_lib or lib()).k3mx_rmsnorm_mx(
-        codes.data_ptr(), scales.data_ptr(), None if sum is None else sum.data_ptr(),
-        None if normed is None else normed.data_ptr(), x.data_ptr(), pitch,
-        None if residual is None else residual.data_ptr(), dt, weight.data_ptr(), eps, rows, cols, _stream(stream)))
+    st = _rmsnorm_mx(codes.data_ptr(), scales.data_ptr(), None if sum is None else sum.data_ptr(),
+                     None if normed is None else normed.data_ptr(), x.data_ptr(), pitch if rows > 1 else cols,
+                     None if residual is None else residual.data_ptr(), dt, weight.data_ptr(), eps, rows, cols,
+                     _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        _check("k3mx_rmsnorm_mx", st)
     return codes, scales
 
 
-def _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, lead):
+def _mx_product_refuse(y, codes, scales, packed, wscales, lead):
     """lead: () for the dense product, (groups,) for the grouped one."""
-    _mx_need(codes, (rows, inner), "codes")
+    rows, inner = _mx_rows(codes, "codes")
     if not isinstance(y, torch.Tensor) or y.dim() != 2 or y.shape[0] != rows or y.shape[1] < 1:
         raise TypeError(f"y: shape [{rows}, out] expected")
     out = y.shape[1]
@@ -568,36 +605,53 @@ def _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, lead):
 def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
     """y [T, out] (float32 or bfloat16) = x w^T: x K3MX_MXFP8 (codes [T, in],
     scales [T, in/32]), w K3MX_MXFP4 (packed [out, in/2], wscales [out, in/32])."""
-    rows, inner, _ = _mx_rows(codes, "codes")
-    out, dt = (y.shape[-1] if y.dim() else 0), _MX_DTYPES.get(y.dtype)
-    if not (dt is not None and y.shape == (rows, out) and y.is_cuda and y.is_contiguous() and inner % 32 == 0 and
-            codes.dtype is _U8 and codes.is_cuda and codes.is_contiguous() and _mx_bytes(scales, (rows, inner // 32)) and
-            _mx_bytes(packed, (out, inner // 2)) and _mx_bytes(wscales, (out, inner // 32))):
-        _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, ())
-    _check("k3mx_mx_linear", (_lib or lib()).k3mx_mx_linear(
-        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(), rows, inner,
-        out, _stream(stream)))
+    try:
+        rows, inner = codes.shape
+        out, dt = y.shape[1], _MX_DTYPES[y.dtype]
+        ok = (y.shape == (rows, out) and scales.shape == (rows, inner // 32) and packed.shape == (out, inner // 2) and
+              wscales.shape == (out, inner // 32) and inner % 32 == 0 and rows and out and
+              codes.dtype is _U8 and scales.dtype is _U8 and packed.dtype is _U8 and wscales.dtype is _U8 and
+              y.is_cuda and codes.is_cuda and scales.is_cuda and packed.is_cuda and wscales.is_cuda and
+              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous() and
+              packed.is_contiguous() and wscales.is_contiguous())
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _mx_product_refuse(y, codes, scales, packed, wscales, ())
+    st = _mx_linear(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(), rows,
+                    inner, out, _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        _check("k3mx_mx_linear", st)
     return y
 
 
 def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
     """k3mx_mx_linear by groups: rows offsets[g]:offsets[g+1] (int32 [groups + 1],
     on the device) with packed[g] [groups, out, in/2], wscales[g]."""
-    rows, inner, _ = _mx_rows(codes, "codes")
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
-        raise TypeError("offsets: shape [groups + 1] expected")
-    groups = offsets.shape[0] - 1
-    out, dt = (y.shape[-1] if y.dim() else 0), _MX_DTYPES.get(y.dtype)
-    if not (dt is not None and y.shape == (rows, out) and y.is_cuda and y.is_contiguous() and inner % 32 == 0 and
-            _mx_bytes(codes, (rows, inner)) and _mx_bytes(scales, (rows, inner // 32)) and
-            _mx_bytes(packed, (groups, out, inner // 2)) and _mx_bytes(wscales, (groups, out, inner // 32)) and
-            offsets.dtype is torch.int32 and offsets.is_cuda and offsets.is_contiguous()):
+    try:
+        rows, inner = codes.shape
+        groups, out, half = packed.shape
+        dt = _MX_DTYPES[y.dtype]
+        ok = (y.shape == (rows, out) and scales.shape == (rows, inner // 32) and half == inner // 2 and
+              wscales.shape == (groups, out, inner // 32) and offsets.shape == (groups + 1,) and
+              inner % 32 == 0 and rows and out and groups and offsets.dtype is torch.int32 and
+              codes.dtype is _U8 and scales.dtype is _U8 and packed.dtype is _U8 and wscales.dtype is _U8 and
+              y.is_cuda and codes.is_cuda and scales.is_cuda and packed.is_cuda and wscales.is_cuda and offsets.is_cuda and
+              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous() and
+              packed.is_contiguous() and wscales.is_contiguous() and offsets.is_contiguous())
+    except (AttributeError, KeyError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise TypeError("offsets: shape [groups + 1] expected")
         if all(isinstance(t, torch.Tensor) and t.is_cuda for t in (y, codes, scales, packed, wscales)):
             _dev(offsets, torch.int32, "offsets")
-        _mx_product_refuse(y, codes, scales, packed, wscales, rows, inner, (groups,))
-    _check("k3mx_mx_grouped", (_lib or lib()).k3mx_mx_grouped(
-        y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(),
-        offsets.data_ptr(), groups, rows, inner, out, _stream(stream)))
+        _mx_product_refuse(y, codes, scales, packed, wscales, (offsets.shape[0] - 1,))
+    st = _mx_grouped(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(),
+                     offsets.data_ptr(), groups, rows, inner, out,
+                     _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        _check("k3mx_mx_grouped", st)
     return y
 
 
