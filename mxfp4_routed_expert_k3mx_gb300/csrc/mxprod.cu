@@ -784,7 +784,13 @@ struct Plan {
     int NT, S, clusters;
 };
 
-// Rows of a unit and CTAs of a cluster.
+// Rows of a unit and CTAs of a cluster: the form whose estimate is least.  Over
+// 67 shapes (rows 1-10587, groups 1-64, out 36-12288, in 128-7168) its choice
+// took 1.7 % longer on the mean than the best of all forms, run-to-run noise
+// included; at the corners 1 x 3584 x 7168 takes 12.7 us with clusters of 1, 8.1
+// with 4 and 9.3 with 8; 64 x 12288 x 7168 16 us in units of 64 rows, 24 in units of
+// 32; 4768 rows of 25 groups (613 x 1664) 10.9 us in units of 256, 13.3 of 128
+// and 23.5 of 32; 926 x 56 x 1280 4.7 us where units of 128 take 5.4.
 Plan choose(const Ctx &c, const ProdArgs &a, int y_bf16) {
     const int groups = a.n_groups < a.n_rows ? a.n_groups : a.n_rows;
     const int mean = (a.n_rows + groups - 1) / groups;       // rows of a group, were they even
