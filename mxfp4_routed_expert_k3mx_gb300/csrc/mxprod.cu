@@ -342,8 +342,6 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     if (S > 1) cluster_sync();               // also: every CTA's barriers are initialised
     else __syncthreads();
     tc_fence_after();
-    if (a.offsets == nullptr) pdl_wait();
-    pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, hd->tmem, 0);
     volatile int *abort_flag = &hd->abort;
 
@@ -367,6 +365,12 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         const uint32_t cnt = goff[lo + 1] - goff[lo], each = cnt / ug, more = cnt - each * ug;
         return Item{lo, (int)mt, goff[lo] + (int)(each * u + min(u, more)), (int)(each + (u < more ? 1 : 0))};
     };
+    // The first item, which is the only one of most short calls, is worked out
+    // here and not by every role: the code of the rest is then never fetched.
+    const Item item0 = n_items > 0 ? item_at(0) : Item{};
+    auto next_item = [&](int k) { return k == 0 ? item0 : item_at(k); };
+    if (a.offsets == nullptr) pdl_wait();
+    pdl_launch_dependents();
     auto fail = [&](int detail) {
         report_status(a.status, kStatusWaitTimeout, detail);
         *abort_flag = 1;
@@ -380,7 +384,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         int issued = 0;
         bool alive = true;                    // as the MMA warp's
         for (int k = 0; k < n_items; k++) {
-            const Item it = item_at(k);
+            const Item it = next_item(k);
             const int rows = (it.ntok + 15) & ~15, wy = it.g * a.out + it.mt * 128;
             const int box = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;          // of the KS = 2 forms
             const CUtensorMap *xmap = rows <= 16 ? &maps.x16 : rows <= 32 ? &maps.x32 : &maps.x64;
@@ -412,7 +416,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     } else if (warp == 1) {
         // ------------------------------------------- the tile's scales --
         auto begin = [&](int k, const uint8_t *(&base)[4]) {
-            const Item it = item_at(k);
+            const Item it = next_item(k);
 #pragma unroll
             for (int r = 0; r < 4; r++)
                 base[r] = a.wscales + ((size_t)it.g * a.out + min(it.mt * 128 + lane + 32 * r, a.out - 1)) * G + 4 * c0;
@@ -452,7 +456,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         // -------------------------------------------- the rows' scales --
         constexpr int R = NT / 32;
         auto begin = [&](int k, const uint8_t *(&base)[R]) {
-            const Item it = item_at(k);
+            const Item it = next_item(k);
 #pragma unroll
             for (int r = 0; r < R; r++)
                 base[r] = a.scales + ((size_t)it.off + min(lane + 32 * r, it.ntok - 1)) * G + 4 * c0;
@@ -491,7 +495,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         auto atom = [&](uint32_t addr16) { return (uint64_t)atom_hi << 32 | (atom_lo + addr16); };
         auto desc = [&](uint32_t addr16) { return (uint64_t)tile_hi << 32 | (tile_lo + addr16); };
         for (int k = 0; k < n_items; k++) {
-            const int rows = __shfl_sync(0xffffffffu, (item_at(k).ntok + 15) & ~15, 0);
+            const int rows = __shfl_sync(0xffffffffu, (next_item(k).ntok + 15) & ~15, 0);
             const uint32_t xstep = KS == 1 ? 0 : rows <= 16 ? 16 * 128 : rows <= 32 ? 32 * 128 : 64 * 128;
             uint32_t id[4];
 #pragma unroll
@@ -563,7 +567,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         // barrier below always has all its warps
         bool alive = true;
         for (int k = 0; k < n_items; k++) {
-            const Item it = item_at(k);
+            const Item it = next_item(k);
             const int n0 = half * HC, n1 = min(it.ntok, n0 + HC);
             // The item's accumulations, added in fp32.  The first is loaded
             // whole (rows past the unit's hold whatever was there) and waited
