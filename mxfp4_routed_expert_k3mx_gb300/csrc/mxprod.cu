@@ -213,6 +213,7 @@ __device__ __forceinline__ void scale_groups_w(int n_items, int kcs, Begin begin
         for (int j = 0; j < kGroup; j++) q[r][j] = 0u;
     int n = 0, i = 0, c = 0;
     if (n_items > 0) load(0, 0);
+#pragma unroll 1
     while (i < n_items) {
         if (!use(n, i, c, q)) return;
         n++;
@@ -231,6 +232,62 @@ __device__ __forceinline__ void scale_groups(int n_items, int kcs, uint32_t bits
     if ((bits & 15) == 0 && kcs % 4 == 0) scale_groups_w<R, 16>(n_items, kcs, begin, use);
     else if ((bits & 7) == 0 && kcs % 2 == 0) scale_groups_w<R, 8>(n_items, kcs, begin, use);
     else scale_groups_w<R, 4>(n_items, kcs, begin, use);
+}
+
+// Every role fetches its own code when a call starts, and beside other kernels
+// it is rarely still in an SM's instruction cache: a one-row and a 64-row
+// product in turn take 19.2 us where each repeated takes 18.5, 22.4 with the
+// three functions below inlined and the loops unrolled (108 to 151 KB of code
+// a kernel, 69 to 115 so).  So what few calls reach is out of line: later
+// items, a wait's polls after the first, dropped blocks.
+
+// Item `it`: groups in order, in a group tile by tile, a tile's units together
+// (they share its weights in L2)
+__device__ __noinline__ Item item_of(const int *ustart, const int *goff, uint32_t it, uint32_t MT, int n_groups) {
+    const uint32_t q = it / MT;
+    int lo = 0, hi = n_groups - 1;                    // last group with ustart <= q
+#pragma unroll 1
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (ustart[m] <= (int)q) lo = m;
+        else hi = m - 1;
+    }
+    const uint32_t u0 = ustart[lo], ug = ustart[lo + 1] - u0, l = it - u0 * MT;
+    const uint32_t mt = l / ug, u = l - mt * ug;
+    // the group's rows in ug units, the first ones a row longer
+    const uint32_t cnt = goff[lo + 1] - goff[lo], each = cnt / ug, more = cnt - each * ug;
+    return Item{lo, (int)mt, goff[lo] + (int)(each * u + min(u, more)), (int)(each + (u < more ? 1 : 0))};
+}
+
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity) {
+    const uint32_t lim = wait_polls();
+    for (uint32_t i = 1; i < lim; i++)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_more(bar, parity);
+}
+
+// The blocks of scale 255 of a group of `n` tiles, v[4][kGroup] the scale words
+// of this lane's rows: codes zeroed once each tile has landed, scales too.
+// False if a wait gave up.
+struct DropAt {
+    uint32_t tfull0, ring, stage;
+    int KS, SA, first, c, n;            // the item's first stage, the group's first tile in it
+};
+__device__ __noinline__ bool drop_blocks(const DropAt d, uint32_t *v, int lane) {
+#pragma unroll 1
+    for (int j = 0; j < kGroup && j < d.n; j++) {
+        const int f = d.first + (d.c + j) / d.KS, s = f % d.SA;
+        if (!mbar_wait(d.tfull0 + 8 * s, (f / d.SA) & 1)) return false;
+#pragma unroll 1
+        for (int r = 0; r < 4; r++) {
+            zero_nan_groups_x128(d.ring + s * d.stage + (d.c + j) % d.KS * kWTile, lane + 32 * r, v[r * kGroup + j]);
+            v[r * kGroup + j] = drop_nan_scales(v[r * kGroup + j]);
+        }
+    }
+    return true;
 }
 
 template <int NT>
@@ -349,22 +406,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     const int n_items = items > first ? (items - first + step - 1) / step : 0;
     const int groups = (kcs + kGroup - 1) / kGroup, n_seg = (groups + seg - 1) / seg;   // accumulations of an item
 
-    // item `first + k * step`: groups in order, in a group tile by tile, a
-    // tile's units together (they share its weights in L2)
-    auto item_at = [&](int k) {
-        const uint32_t it = first + k * step, q = it / (uint32_t)MT;
-        int lo = 0, hi = a.n_groups - 1;                    // last group with ustart <= q
-        while (lo < hi) {
-            const int m = (lo + hi + 1) >> 1;
-            if (ustart[m] <= (int)q) lo = m;
-            else hi = m - 1;
-        }
-        const uint32_t u0 = ustart[lo], ug = ustart[lo + 1] - u0, l = it - u0 * MT;
-        const uint32_t mt = l / ug, u = l - mt * ug;
-        // the group's rows in ug units, the first ones a row longer
-        const uint32_t cnt = goff[lo + 1] - goff[lo], each = cnt / ug, more = cnt - each * ug;
-        return Item{lo, (int)mt, goff[lo] + (int)(each * u + min(u, more)), (int)(each + (u < more ? 1 : 0))};
-    };
+    auto item_at = [&](int k) { return item_of(ustart, goff, first + k * step, MT, a.n_groups); };
     // The first item, which is the only one of most short calls, is worked out
     // here and not by every role: the code of the rest is then never fetched.
     const Item item0 = n_items > 0 ? item_at(0) : Item{};
@@ -383,14 +425,16 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         Slot<SA> sl;
         int issued = 0;
         bool alive = true;                    // as the MMA warp's
+#pragma unroll 1
         for (int k = 0; k < n_items; k++) {
             const Item it = next_item(k);
             const int rows = (it.ntok + 15) & ~15, wy = it.g * a.out + it.mt * 128;
             const int box = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;          // of the KS = 2 forms
             const CUtensorMap *xmap = rows <= 16 ? &maps.x16 : rows <= 32 ? &maps.x32 : &maps.x64;
+#pragma unroll 1
             for (int c = c0; c < c0 + kcs; c += KS, sl.next()) {
                 const uint32_t bar = tfull0 + 8 * sl.i, st = ring + sl.i * Sh::STAGE, xt = st + KS * kWTile;
-                alive = alive && mbar_wait(empty0 + 8 * sl.i, sl.ph ^ 1);
+                alive = alive && wait_for(empty0 + 8 * sl.i, sl.ph ^ 1);
                 if (leader && alive) {
                     if (KS == 2) {
                         mbar_arrive_expect_tx(bar, 2 * (kWTileTx + box * 128));
@@ -400,7 +444,9 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                         mbar_arrive_expect_tx(bar, kWTileTx + rows * 128);
                         tma_3d(st, &maps.w, 0, wy, c, bar, wpol);
                         int r = 0;
+#pragma unroll 1
                         for (; r + 64 <= rows; r += 64) tma_3d(xt + r * 128, &maps.x64, 0, it.off + r, c, bar, xpol);
+#pragma unroll 1
                         for (; r < rows; r += 16) tma_3d(xt + r * 128, &maps.x16, 0, it.off + r, c, bar, xpol);
                     }
                     issued++;
@@ -423,30 +469,33 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         };
         auto use = [&](int n, int i, int c, const uint32_t (&w)[4][kGroup]) {
             const int gs = n % SG;
-            if (*abort_flag || !mbar_wait(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
+            if (*abort_flag || !wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
                 if (lane == 0) fail(410);
                 return false;
             }
-            uint32_t nan = 0;
+            uint32_t v[4][kGroup], nan = 0;
 #pragma unroll
             for (int r = 0; r < 4; r++)
 #pragma unroll
-                for (int j = 0; j < kGroup; j++) nan |= nan_scale_mask(w[r][j]);
-            const bool drop = __any_sync(0xffffffffu, nan != 0);        // rare
-#pragma unroll
-            for (int j = 0; j < kGroup; j++) {
-                if (drop && c + j < kcs) {
-                    const int f = i * fts + (c + j) / KS, s = f % SA;
-                    if (!mbar_wait(tfull0 + 8 * s, (f / SA) & 1)) {
-                        if (lane == 0) fail(411);
-                        return false;
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; r++) zero_nan_groups_x128(ring + s * Sh::STAGE + (c + j) % KS * kWTile, lane + 32 * r, w[r][j]);
+                for (int j = 0; j < kGroup; j++) {
+                    v[r][j] = w[r][j];
+                    nan |= (~v[r][j] - 0x01010101u) & v[r][j] & 0x80808080u;      // a byte of ~v is 0
                 }
-                sts128(sgroups + gs * Sh::GROUP + j * kAtom + 16 * lane, drop_nan_scales(w[0][j]),
-                       drop_nan_scales(w[1][j]), drop_nan_scales(w[2][j]), drop_nan_scales(w[3][j]));
+            if (__any_sync(0xffffffffu, nan != 0)) {
+                const DropAt at{tfull0, ring, Sh::STAGE, KS, SA, i * fts, c, kcs - c};
+                uint32_t u[4 * kGroup];
+#pragma unroll
+                for (int t = 0; t < 4 * kGroup; t++) u[t] = v[t / kGroup][t % kGroup];
+                if (!drop_blocks(at, u, lane)) {
+                    if (lane == 0) fail(411);
+                    return false;
+                }
+#pragma unroll
+                for (int t = 0; t < 4 * kGroup; t++) v[t / kGroup][t % kGroup] = u[t];
             }
+#pragma unroll
+            for (int j = 0; j < kGroup; j++)
+                sts128(sgroups + gs * Sh::GROUP + j * kAtom + 16 * lane, v[0][j], v[1][j], v[2][j], v[3][j]);
             fence_async_smem();
             mbar_arrive(gfull0 + 8 * gs);
             return true;
@@ -463,7 +512,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         };
         auto use = [&](int n, int, int, const uint32_t (&w)[R][kGroup]) {
             const int gs = n % SG;
-            if (*abort_flag || !mbar_wait(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
+            if (*abort_flag || !wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
                 if (lane == 0) fail(420);
                 return false;
             }
@@ -494,6 +543,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         const uint32_t atom_hi = (uint32_t)(desc_atom(0, 128) >> 32), atom_lo = (uint32_t)desc_atom(0, 128);
         auto atom = [&](uint32_t addr16) { return (uint64_t)atom_hi << 32 | (atom_lo + addr16); };
         auto desc = [&](uint32_t addr16) { return (uint64_t)tile_hi << 32 | (tile_lo + addr16); };
+#pragma unroll 1
         for (int k = 0; k < n_items; k++) {
             const int rows = __shfl_sync(0xffffffffu, (next_item(k).ntok + 15) & ~15, 0);
             const uint32_t xstep = KS == 1 ? 0 : rows <= 16 ? 16 * 128 : rows <= 32 ? 32 * 128 : 64 * 128;
@@ -501,9 +551,10 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
             for (int ks = 0; ks < 4; ks++) id[ks] = idesc_e2m1_e4m3(rows, ks);
             int in_seg = 0;
+#pragma unroll 1
             for (int c = 0; c < kcs; c += kGroup) {
-                if (in_seg == 0) alive = alive && mbar_wait(acce0 + 8 * sb.i, sb.ph ^ 1);
-                alive = alive && mbar_wait(gfull0 + 8 * sg.i, sg.ph);
+                if (in_seg == 0) alive = alive && wait_for(acce0 + 8 * sb.i, sb.ph ^ 1);
+                alive = alive && wait_for(gfull0 + 8 * sg.i, sg.ph);
                 const bool last = c + kGroup >= kcs, seg_end = last || in_seg + 1 == seg;
                 const uint32_t d = tmem + sb.i * NT;
                 const uint32_t sf = tmem + Sh::SF_COL + sg.i * (kGroup * Sh::SF_STEP);
@@ -511,7 +562,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
 #pragma unroll
                 for (int j = 0; j < kGroup; j += KS) {
                     if (c + j < kcs) {
-                        alive = alive && (ready || mbar_wait(tfull0 + 8 * sl.i, sl.ph));
+                        alive = alive && (ready || wait_for(tfull0 + 8 * sl.i, sl.ph));
                         const uint32_t slot = sl.i;
                         sl.next();
                         ready = mbar_test(tfull0 + 8 * sl.i, sl.ph);
@@ -566,6 +617,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         // `alive` as in the MMA warp: the loops run to their ends, so the named
         // barrier below always has all its warps
         bool alive = true;
+#pragma unroll 1
         for (int k = 0; k < n_items; k++) {
             const Item it = next_item(k);
             const int n0 = half * HC, n1 = min(it.ntok, n0 + HC);
@@ -573,7 +625,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             // whole (rows past the unit's hold whatever was there) and waited
             // for once.
             float v[HC];
-            alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
+            alive = alive && wait_for(accf0 + 8 * sb.i, sb.ph);
             __syncwarp();                       // (each lane polls for itself; the loads are the whole warp's)
             tc_fence_after();
 #pragma unroll
@@ -582,8 +634,9 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             tc_fence_before();
             mbar_arrive(acce0 + 8 * sb.i);
             sb.next();
+#pragma unroll 1
             for (int sg = 1; sg < n_seg; sg++, sb.next()) {
-                alive = alive && mbar_wait(accf0 + 8 * sb.i, sb.ph);
+                alive = alive && wait_for(accf0 + 8 * sb.i, sb.ph);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
@@ -653,9 +706,11 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     alive = alive && wait_cluster(bar, ex.ph);
                     __syncwarp();
                     const float *src = reinterpret_cast<const float *>(red + ex.i * kExBytes);
+#pragma unroll 1
                     for (int i = tid - kEpi0 * 32; i < RS * (cols / 4); i += kEpiThreads) {
                         const int n = i / RS * 4, r = i % RS, out = it.mt * 128 + rank * RS + r;
                         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
                         for (int s = 0; s < S; s++) {
                             const float4 q = *reinterpret_cast<const float4 *>(src + (s * RS + r) * kExPitch + n);
                             sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
