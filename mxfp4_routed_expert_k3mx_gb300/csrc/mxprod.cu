@@ -469,7 +469,8 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         };
         auto use = [&](int n, int i, int c, const uint32_t (&w)[4][kGroup]) {
             const int gs = n % SG;
-            if (*abort_flag || !wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
+            // (lanes poll for themselves: they leave together, for the votes below)
+            if (!__all_sync(0xffffffffu, !*abort_flag && wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1))) {
                 if (lane == 0) fail(410);
                 return false;
             }
@@ -486,7 +487,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                 uint32_t u[4 * kGroup];
 #pragma unroll
                 for (int t = 0; t < 4 * kGroup; t++) u[t] = v[t / kGroup][t % kGroup];
-                if (!drop_blocks(at, u, lane)) {
+                if (!__all_sync(0xffffffffu, drop_blocks(at, u, lane))) {
                     if (lane == 0) fail(411);
                     return false;
                 }
@@ -512,7 +513,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         };
         auto use = [&](int n, int, int, const uint32_t (&w)[R][kGroup]) {
             const int gs = n % SG;
-            if (*abort_flag || !wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1)) {
+            if (!__all_sync(0xffffffffu, !*abort_flag && wait_for(gempty0 + 8 * gs, ((n / SG) & 1) ^ 1))) {
                 if (lane == 0) fail(420);
                 return false;
             }
@@ -735,7 +736,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             }
             if (*abort_flag) alive = false;
         }
-        if (!alive && lane == 0) fail(440);
+        if (__any_sync(0xffffffffu, !alive) && lane == 0) fail(440);
     }
 
     __syncthreads();

@@ -296,6 +296,34 @@ def test_product_waits_are_bounded(cuda_dev, rows, inner, out):
     assert torch.equal(y, clean)
 
 
+@pytest.mark.parametrize("rows", [2, 40, 300])
+def test_waits_for_dropped_blocks_are_bounded(cuda_dev, rows):
+    """The same where every fourth block is dropped, so that the scales' warp
+    also waits for tiles: whichever wait gives up, the call ends, and the next
+    one with the limit restored is right."""
+    xc, xs, p, ws = inputs(rows, 65536, (300,), rows)
+    ws[:, ::4] = 255
+    d = dev(xc, xs, p, ws)
+    clean = torch.empty(rows, 300, dtype=BF16, device="cuda:0")
+    k3mx.k3mx_mx_linear(clean, *d)
+    assert k3mx.k3mx_device_status() == (0, 0)
+    y = torch.empty_like(clean)
+    k3mx.k3mx_set_wait_limit(1)
+    try:
+        seen = set()
+        for _ in range(20):
+            k3mx.k3mx_mx_linear(y, *d)
+            seen.add(k3mx.k3mx_device_status())
+    finally:
+        k3mx.k3mx_set_wait_limit(0)
+    assert all(st == 0 or st == 6 and 400 <= detail < 460 for st, detail in seen), seen
+    assert any(st == 6 for st, _ in seen), "no wait ran out"
+    y.fill_(0)
+    k3mx.k3mx_mx_linear(y, *d)
+    assert k3mx.k3mx_device_status() == (0, 0)
+    assert torch.equal(y, clean)
+
+
 # ------------------------------------------------- offsets past 32 bits --
 
 def test_grouped_weights_past_4_gib(cuda_dev):
