@@ -4,8 +4,21 @@
 //
 // A block of 32 columns is four neighbouring lanes of 8 values, so its
 // largest magnitude is 8 compares and two shuffles, and every load and store
-// is a whole vector.  All three kernels are bound by HBM: one pass over the
-// input, one over each output.
+// is a whole vector.  All three kernels make one pass over the input and one
+// over each output.  Measured (repeated calls, inputs larger than L2, of a
+// measured copy of 6.77 TB/s):
+//   quantise 12288 x 7168 fp32 to MXFP4    56.9 us, 7.0 TB/s; back 58.7 us, 6.8
+//   quantise 4096 x 7168 bf16 to MXFP8     14.8 us, 6.0 TB/s; back 15.0 us, 5.9
+//   norm 4096 x 7168 fp32, no normed       59.4 us, 6.4 TB/s
+//   norm 4096 x 7168 bf16, with normed     49.0 us, 5.4 TB/s; without 44.6, 4.6
+//   one row of 7168 bf16: quantise 1.3 us, back 1.2, norm 2.9 (launch and one
+//   or two memory latencies)
+// The large fp32 calls are bound by HBM.  The bf16 norm has half the bytes for
+// the same values, and the latencies of a row (load, sum, weights, stores) are
+// not all hidden by the rows beside it: rows streamed through shared memory
+// by bulk copies took 36.5 us without normed where this form took 42.7 at the
+// time, but 46.8 and 47.1 with it, 63.8 and 59.1 in fp32, and 31 and 26.4 for
+// 8192 x 2048.
 #include "mxops.cuh"
 #include "pieces.cuh"
 
@@ -119,12 +132,17 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8]) {
     return w;
 }
 
+// largest of three magnitudes, NaN if one is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 // largest |v| of the block (four lanes x 8 values) as fp32 bits: non-negative
 // floats order as their bit patterns, Inf and NaN above every finite value
 __device__ __forceinline__ uint32_t block_max(const float (&v)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(fabsf(v[j])));
+    const float a = max_abs3(v[0], v[1], v[2]), b = max_abs3(v[3], v[4], v[5]);
+    uint32_t m = __float_as_uint(max_abs3(a, b, max_abs3(v[6], v[7], v[7]))) & 0x7FFFFFFFu;
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
@@ -137,11 +155,16 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], uint8_t *codes, uint8
     const uint32_t s = block_scale<FMT>(block_max(v), down);
     // 2^-e times a value is exact (or, for the smallest values, below half
     // the smallest code); a dropped block's codes are zero
+    const uint32_t keep = s == 255u ? 0u : 0xFFFFFFFFu;
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = s == 255u ? 0.f : v[j] * down;
+    for (int j = 0; j < 8; j++) v[j] *= down;
     if (live) {
-        if (FMT == K3MX_MXFP4) reinterpret_cast<uint32_t *>(codes)[q8] = to_e2m1x8(v);
-        else reinterpret_cast<uint2 *>(codes)[q8] = to_e4m3x8(v);
+        if (FMT == K3MX_MXFP4) {
+            reinterpret_cast<uint32_t *>(codes)[q8] = to_e2m1x8(v) & keep;
+        } else {
+            const uint2 w = to_e4m3x8(v);
+            reinterpret_cast<uint2 *>(codes)[q8] = make_uint2(w.x & keep, w.y & keep);
+        }
         if ((q8 & 3) == 0) scales[q8 >> 2] = (uint8_t)s;
     }
     return s;
@@ -233,6 +256,56 @@ k_mx_dequantize(void *y, const uint8_t *__restrict__ codes, const uint8_t *__res
 
 // ------------------------------------------------------------------ norm --
 
+// A sum as s + l, l what s was rounded by.
+__device__ __forceinline__ void two_sum(float &s, float &l, float a) {
+    const float t = s + a, b = t - s;
+    l += (s - (t - b)) + (a - b);
+    s = t;
+}
+// s + l of all lanes, or of every `lanes` of them (a power of two), in the same
+// order on each
+__device__ __forceinline__ void warp_two_sum(float &s, float &l, int lanes) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) {
+            const float s2 = __shfl_xor_sync(0xffffffffu, s, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+            l += l2;
+            two_sum(s, l, s2);
+        }
+}
+
+// The factor of a row whose squares sum to ss + sl: 1 / sqrt(sum / width + eps)
+// as k + kl.
+__device__ __forceinline__ void norm_factor(float ss, float sl, int width, float eps, float &k, float &kl) {
+    const float w = (float)width, q = ss / w, m = q + eps, b = m - q;
+    const float ml = ((q - (m - b)) + (eps - b)) + (fmaf(-q, w, ss) + sl) / w;      // what q and m were rounded by
+    k = rsqrtf(m);
+    const float k2 = k * k;
+    kl = 0.5f * k * (fmaf(-m, k2, 1.0f) - m * fmaf(k, k, -k2) - ml * k2);
+    if (!(m > 0.f && m < INFINITY)) kl = 0.f;
+}
+
+// Eight values times g (k + kl), so that rounding them on to e4m3 or bf16
+// rounds the exact products: k's upper 16 bits times g are exact, the rest is
+// added in the one rounding, and that goes to the odd one of the two fp32
+// neighbours (where the product is none itself), which is never the middle of
+// two codes (two directed roundings and a choice: 4096 x 7168 bf16 in 49.9 us,
+// 48.3 rounded to the nearest; finding the few doubtful products and mending
+// them in a branch took 60).
+__device__ __forceinline__ void scale8(float (&v)[8], uint4 g, float k, float kl) {
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+    const float kh = __uint_as_float(__float_as_uint(k) & 0xFFFFFF00u);
+    kl += k - kh;
+    k = kh;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float gj = __uint_as_float(j & 1 ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
+        const float gk = gj * k, rest = v[j] * (gj * kl);
+        const float down = __fmaf_rd(v[j], gk, rest), up = __fmaf_ru(v[j], gk, rest);
+        v[j] = __float_as_uint(down) & 1u ? down : up;
+    }
+}
+
 // V runs of 8 values a thread, the row in registers between its two uses (the
 // sum of squares, then the scaled values): every input is read once, all
 // loads of a row at the start.  WARP: a row to a warp, four rows to a CTA of
@@ -279,41 +352,35 @@ __global__ void __launch_bounds__(WARP ? 128 : V == 1 ? 1024 : V == 2 ? 512 : 10
             store8<BF16>(a.sum, t * a.width + 8 * (p * P + i0), v[p], p * P + i0 < per_row);
         }
     }
-    float ss = 0.f;
+    // Where many roundings average out (a thread's four parts, a warp's lanes)
+    // the sum is plain fp32; where each would be the whole sum's, the low half
+    // is kept.
+    float sq[4] = {};
 #pragma unroll
     for (int p = 0; p < V; p++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) ss = fmaf(v[p][j], v[p][j], ss);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!WARP) {
-        if (lane == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        ss = lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f;
+        for (int j = 0; j < 8; j++) sq[j & 3] = fmaf(v[p][j], v[p][j], sq[j & 3]);
+    float ss = (sq[0] + sq[1]) + (sq[2] + sq[3]), sl = 0.f;
+    if (WARP) {
+        warp_two_sum(ss, sl, 32);
+    } else {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) part[threadIdx.x >> 5] = ss;
+        __syncthreads();
+        const int nw = blockDim.x >> 5, lanes = nw == 1 ? 1 : 1 << (32 - __clz(nw - 1));
+        ss = (lane & (lanes - 1)) < nw ? part[lane & (lanes - 1)] : 0.f;
+        warp_two_sum(ss, sl, lanes);
     }
-    // 1 / sqrt(mean + eps) as k + kl, and below g times that as gk + gl, so that
-    // a value is rounded once: one near the middle of two codes then goes the
-    // way the exact one does unless it is within about 2^-24 of it.
-    const float w = (float)a.width, q = ss / w, m = q + a.eps;
-    const float ml = ((q - m) + a.eps) + fmaf(-q, w, ss) / w;         // what q and m were rounded by
-    const float k = rsqrtf(m), k2 = k * k;
-    float kl = 0.5f * k * (fmaf(-m, k2, 1.0f) - m * fmaf(k, k, -k2) - ml * k2);
-    if (!(m > 0.f && m < INFINITY)) kl = 0.f;
+    float k, kl;
+    norm_factor(ss, sl, a.width, a.eps, k, kl);
 #pragma unroll
     for (int p = 0; p < V; p++) {
         const int i = p * P + i0;
         const bool live = i < per_row;
         if (!EARLY) weights(p);
-        const uint32_t gw[4] = {gq[p].x, gq[p].y, gq[p].z, gq[p].w};
         if (live) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float g = __uint_as_float(j & 1 ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
-                const float gk = g * k, gl = fmaf(g, kl, fmaf(g, k, -gk));
-                v[p][j] = fmaf(v[p][j], gk, v[p][j] * gl);
-            }
+            scale8(v[p], gq[p], k, kl);
             if (a.normed != nullptr) store8<true>(a.normed, t * a.width + 8 * i, v[p], true);
         }
         encode8<K3MX_MXFP8>(v[p], a.codes, a.scales, t * per_row + i, live);

@@ -185,6 +185,35 @@ def test_norm_forms(cuda_dev, dtype):
     check_norm(big, big.flip(0).contiguous(), w[:96].contiguous(), 1e-5)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,d", [(700, 64), (40, 1120), (1300, 512), (20, 7168), (300, 7168), (1000, 7168), (9, 16384)])
+def test_norm_codes_are_the_exact_ones(cuda_dev, dtype, t, d):
+    """Sums that fp32 holds, so that only the norm rounds: its sum of squares,
+    by at most fifteen roundings of 2^-24 (a thread's eight squares to a part, its
+    parts' two levels, a warp's five), halved by the root: every code and scale
+    is the exact norm's within 2^-20.  Those are roundings of parts and average
+    out to 2^-27 and less: of codes 0.09 apart, one in several million goes the
+    other way.  One in 10^6 is allowed, and of bf16 values, 0.004 apart, 20."""
+    g = torch.Generator(device=cuda_dev).manual_seed(t + d)
+    x = torch.randn(t, d, generator=g, device=cuda_dev)
+    r = 4 * torch.randn(t, d, generator=g, device=cuda_dev)
+    x, r = ((128 * v).round().clamp(-255, 255).div(128).to(dtype) for v in (x, r))
+    w = (1 + 0.1 * torch.randn(d, generator=g, device=cuda_dev)).to(BF16)
+    eps = 2.0 ** -17
+    check_norm(x, r, w, eps, normed=False)
+    codes, scales, _, normed = run_norm(x, r, w, eps)
+    bare = run_norm(x, r, w, eps, normed=False)
+    assert torch.equal(codes, bare[0]) and torch.equal(scales, bare[1])
+    s = x.double() + r.double()
+    n = (s / torch.sqrt(s.square().mean(1, keepdim=True) + eps) * w.double()).cpu().numpy()
+    code, sb = mx_ref.quantize(n, mx_ref.MXFP8)
+    off = np.count_nonzero(codes.cpu().numpy() != code)
+    f, e = np.frexp(n)
+    off16 = np.count_nonzero(normed.double().cpu().numpy() != np.ldexp(np.rint(f * 256), e - 8))
+    assert np.array_equal(scales.cpu().numpy(), sb)
+    assert off <= 1 + 1e-6 * n.size and off16 <= 2 + 2e-5 * n.size
+
+
 def test_norm_of_nan_row_is_nan_blocks(cuda_dev):
     x = torch.randn(4, 256, device=cuda_dev)
     x[1, 7] = float("nan")
