@@ -33,7 +33,7 @@
 // Measured (repeated calls; of a measured copy of 6.77 TB/s and library bf16 of
 // 1957 TFLOP/s in a burst):
 //   1 x 3584 x 7168 bf16 (rows, out, in)      7.5 us, 1.8 TB/s of weights and scales
-//   1 x 12288 x 7168 bf16                    13.1 us, 3.6 TB/s; 1 x 19456 x 7168 14.8, 5.0
+//   1 x 12288 x 7168 bf16                    13.1 us, 3.6 TB/s; 1 x 19456 x 7168 14.4, 5.1
 //   16 rows of 64 groups, 2048 x 3584 bf16   16.2 us, 3.6 TB/s
 //   64 x 12288 x 7168 fp32                   15.9 us, 3.2 TB/s, 710 TFLOP/s
 //   4096 x 12288 x 7168 bf16                 214 us, 3370 TFLOP/s (258 us where the
