@@ -7,6 +7,7 @@ device pointers.  PyTorch provides device memory and streams.  There is no
 CPU fallback: importing this package without a built library raises.
 """
 import ctypes
+import importlib.util
 import os
 import re
 
@@ -435,21 +436,38 @@ def k3mx_moe_routed_host(y_host, x_host, experts, logits_host, bias_host, worksp
 # ------------------------------------------------ microscaled operators --
 #
 # One-token calls last a few microseconds on the device, and the host's share
-# of a call is of that size.  So each function asks in one expression, with
-# no call of its own, whether its arguments are as they should be, and only
-# where they are not looks for what is wrong and names it.
+# of a call is of that size.  So a module in C++ (csrc/binding.cpp) asks
+# whether the arguments are as they should be and calls the C function; only
+# where they are not, the functions here look for what is wrong and name it.
 
+_MX_FUNCS = ("k3mx_mx_quantize", "k3mx_mx_dequantize", "k3mx_rmsnorm_mx", "k3mx_mx_linear", "k3mx_mx_grouped")
 _MX_DTYPES = {torch.float32: K3MX_F32, torch.bfloat16: K3MX_BF16}
-_U8, _BF16 = torch.uint8, torch.bfloat16
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_U8 = torch.uint8
+
+
+def _load_binding():
+    """Puts the module's functions, bound to the library's, in the places of
+    the ones below."""
+    path = _build.BINDING
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+    spec = importlib.util.spec_from_file_location("_k3mx_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in _MX_FUNCS))
+    for name in _MX_FUNCS:
+        globals()[name[len("k3mx"):]] = getattr(module, name[len("k3mx_"):])
 
 
 def _entry(name):
-    """A C function by name, put in this module's place for it at its first call."""
+    """A function of the binding by name, there from its first call on."""
     def first(*args):
-        func = globals()[name[len("k3mx"):]] = getattr(lib(), name)
-        return func(*args)
+        _load_binding()
+        return globals()[name](*args)
     return first
+
+
+_mx_quantize, _mx_dequantize, _rmsnorm_mx, _mx_linear, _mx_grouped = (_entry(n[len("k3mx"):]) for n in _MX_FUNCS)
 
 
 def _mx_need(t, shape, name):
@@ -490,60 +508,30 @@ def _mx_refuse(rows, cols, fmt, shapes, bytes_, values, strided=None):
     raise TypeError("arguments of unexpected type, device or layout")
 
 
-_mx_quantize = _entry("k3mx_mx_quantize")
-_mx_dequantize = _entry("k3mx_mx_dequantize")
-_rmsnorm_mx = _entry("k3mx_rmsnorm_mx")
-_mx_linear = _entry("k3mx_mx_linear")
-_mx_grouped = _entry("k3mx_mx_grouped")
-
-
 def k3mx_mx_quantize(codes, scales, x, fmt, stream=None):
     """x [rows, cols] (float32 or bfloat16, rows may be strided) to microscaled
     codes (uint8 [rows, cols/2] for K3MX_MXFP4, [rows, cols] for K3MX_MXFP8)
     and scale bytes (uint8 [rows, cols/32])."""
-    try:
-        rows, cols = x.shape
-        dt = _MX_DTYPES[x.dtype]
-        pitch = cols if x.is_contiguous() else x.stride(0) if x.stride(1) == 1 else -1
-        ok = (codes.shape == (rows, cols if fmt == 1 else cols // 2) and scales.shape == (rows, cols // 32) and
-              (fmt == 1 or fmt == 0) and cols % 32 == 0 and rows and (pitch >= cols or rows == 1 and pitch >= 0) and
-              codes.dtype is _U8 and scales.dtype is _U8 and x.is_cuda and codes.is_cuda and scales.is_cuda and
-              codes.is_contiguous() and scales.is_contiguous())
-    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = _mx_quantize(codes, scales, x, fmt, stream if stream is None else _stream(stream))
+    if st < 0:
         rows, cols = _mx_rows(x, "x")
         _mx_refuse(rows, cols, fmt, [(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), "codes"),
                                      (scales, (rows, cols // 32), "scales")],
                    [(codes, "codes"), (scales, "scales")], [], strided=(x, "x"))
-    st = _mx_quantize(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), dt, rows, cols, pitch if rows > 1 else cols, fmt,
-                      _raw_stream(_device()) if stream is None else _stream(stream))
-    if st:
-        _check("k3mx_mx_quantize", st)
+    _check("k3mx_mx_quantize", st)
     return codes, scales
 
 
 def k3mx_mx_dequantize(y, codes, scales, fmt, stream=None):
     """The values that codes and scale bytes stand for, in y [rows, cols]
     (float32: exact; bfloat16: rounded to nearest)."""
-    try:
-        rows, cols = y.shape
-        dt = _MX_DTYPES[y.dtype]
-        ok = (codes.shape == (rows, cols if fmt == 1 else cols // 2) and scales.shape == (rows, cols // 32) and
-              (fmt == 1 or fmt == 0) and cols % 32 == 0 and rows and codes.dtype is _U8 and scales.dtype is _U8 and
-              y.is_cuda and codes.is_cuda and scales.is_cuda and
-              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous())
-    except (AttributeError, KeyError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = _mx_dequantize(y, codes, scales, fmt, stream if stream is None else _stream(stream))
+    if st < 0:
         rows, cols = _mx_rows(y, "y")
         _mx_refuse(rows, cols, fmt, [(codes, (rows, cols // 2 if fmt == K3MX_MXFP4 else cols), "codes"),
                                      (scales, (rows, cols // 32), "scales")],
                    [(codes, "codes"), (scales, "scales")], [(y, "y")])
-    st = _mx_dequantize(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), rows, cols, fmt,
-                        _raw_stream(_device()) if stream is None else _stream(stream))
-    if st:
-        _check("k3mx_mx_dequantize", st)
+    _check("k3mx_mx_dequantize", st)
     return y
 
 
@@ -553,23 +541,8 @@ def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, s
     float32 or bfloat16 (rows may be strided), residual and sum of the same
     type (both None: no residual; sum may be residual itself), weight
     bfloat16 [width]."""
-    try:
-        wide = rows, cols = tuple(x.shape)
-        dt, kind = _MX_DTYPES[x.dtype], x.dtype
-        pitch = cols if x.is_contiguous() else x.stride(0) if x.stride(1) == 1 else -1
-        ok = (codes.shape == wide and scales.shape == (rows, cols // 32) and weight.shape == (cols,) and
-              cols % 32 == 0 and rows and (pitch >= cols or rows == 1 and pitch >= 0) and
-              codes.dtype is _U8 and scales.dtype is _U8 and weight.dtype is _BF16 and
-              x.is_cuda and codes.is_cuda and scales.is_cuda and weight.is_cuda and
-              codes.is_contiguous() and scales.is_contiguous() and weight.is_contiguous() and
-              (residual is None and sum is None or
-               residual.shape == wide and sum.shape == wide and residual.dtype is kind and sum.dtype is kind and
-               residual.is_cuda and sum.is_cuda and residual.is_contiguous() and sum.is_contiguous()) and
-              (normed is None or normed.shape == wide and normed.dtype is _BF16 and normed.is_cuda and
-               normed.is_contiguous()))
-    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = _rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed, stream if stream is None else _stream(stream))
+    if st < 0:
         rows, cols = _mx_rows(x, "x")
         if (residual is None) != (sum is None):
             raise TypeError("sum: expected exactly where residual is given (shape of x)")
@@ -578,15 +551,10 @@ def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, s
         for t, shape, n in (shapes + [(t, (rows, cols), n) for t, n in given] +
                             ([(normed, (rows, cols), "normed")] if normed is not None else [])):
             _mx_need(t, shape, n)
-        _dev(weight, _BF16, "weight")
-        _dev_opt(normed, _BF16, "normed")
+        _dev(weight, torch.bfloat16, "weight")
+        _dev_opt(normed, torch.bfloat16, "normed")
         _mx_refuse(rows, cols, K3MX_MXFP8, [], [(codes, "codes"), (scales, "scales")], given, strided=(x, "x"))
-    st = _rmsnorm_mx(codes.data_ptr(), scales.data_ptr(), None if sum is None else sum.data_ptr(),
-                     None if normed is None else normed.data_ptr(), x.data_ptr(), pitch if rows > 1 else cols,
-                     None if residual is None else residual.data_ptr(), dt, weight.data_ptr(), eps, rows, cols,
-                     _raw_stream(_device()) if stream is None else _stream(stream))
-    if st:
-        _check("k3mx_rmsnorm_mx", st)
+    _check("k3mx_rmsnorm_mx", st)
     return codes, scales
 
 
@@ -605,53 +573,24 @@ def _mx_product_refuse(y, codes, scales, packed, wscales, lead):
 def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
     """y [T, out] (float32 or bfloat16) = x w^T: x K3MX_MXFP8 (codes [T, in],
     scales [T, in/32]), w K3MX_MXFP4 (packed [out, in/2], wscales [out, in/32])."""
-    try:
-        rows, inner = codes.shape
-        out, dt = y.shape[1], _MX_DTYPES[y.dtype]
-        ok = (y.shape == (rows, out) and scales.shape == (rows, inner // 32) and packed.shape == (out, inner // 2) and
-              wscales.shape == (out, inner // 32) and inner % 32 == 0 and rows and out and
-              codes.dtype is _U8 and scales.dtype is _U8 and packed.dtype is _U8 and wscales.dtype is _U8 and
-              y.is_cuda and codes.is_cuda and scales.is_cuda and packed.is_cuda and wscales.is_cuda and
-              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous() and
-              packed.is_contiguous() and wscales.is_contiguous())
-    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = _mx_linear(y, codes, scales, packed, wscales, stream if stream is None else _stream(stream))
+    if st < 0:
         _mx_product_refuse(y, codes, scales, packed, wscales, ())
-    st = _mx_linear(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(), rows,
-                    inner, out, _raw_stream(_device()) if stream is None else _stream(stream))
-    if st:
-        _check("k3mx_mx_linear", st)
+    _check("k3mx_mx_linear", st)
     return y
 
 
 def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
     """k3mx_mx_linear by groups: rows offsets[g]:offsets[g+1] (int32 [groups + 1],
     on the device) with packed[g] [groups, out, in/2], wscales[g]."""
-    try:
-        rows, inner = codes.shape
-        groups, out, half = packed.shape
-        dt = _MX_DTYPES[y.dtype]
-        ok = (y.shape == (rows, out) and scales.shape == (rows, inner // 32) and half == inner // 2 and
-              wscales.shape == (groups, out, inner // 32) and offsets.shape == (groups + 1,) and
-              inner % 32 == 0 and rows and out and groups and offsets.dtype is torch.int32 and
-              codes.dtype is _U8 and scales.dtype is _U8 and packed.dtype is _U8 and wscales.dtype is _U8 and
-              y.is_cuda and codes.is_cuda and scales.is_cuda and packed.is_cuda and wscales.is_cuda and offsets.is_cuda and
-              y.is_contiguous() and codes.is_contiguous() and scales.is_contiguous() and
-              packed.is_contiguous() and wscales.is_contiguous() and offsets.is_contiguous())
-    except (AttributeError, KeyError, TypeError, ValueError):
-        ok = False
-    if not ok:
+    st = _mx_grouped(y, codes, scales, packed, wscales, offsets, stream if stream is None else _stream(stream))
+    if st < 0:
         if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
             raise TypeError("offsets: shape [groups + 1] expected")
         if all(isinstance(t, torch.Tensor) and t.is_cuda for t in (y, codes, scales, packed, wscales)):
             _dev(offsets, torch.int32, "offsets")
         _mx_product_refuse(y, codes, scales, packed, wscales, (offsets.shape[0] - 1,))
-    st = _mx_grouped(y.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(), packed.data_ptr(), wscales.data_ptr(),
-                     offsets.data_ptr(), groups, rows, inner, out,
-                     _raw_stream(_device()) if stream is None else _stream(stream))
-    if st:
-        _check("k3mx_mx_grouped", st)
+    _check("k3mx_mx_grouped", st)
     return y
 
 

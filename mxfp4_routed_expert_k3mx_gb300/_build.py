@@ -2,12 +2,18 @@
 
 Each .cu file compiles to its own object in parallel; the objects link into
 one shared library next to this file.  Rebuilds only when a source or header
-is newer than the library.
+is newer than the library.  csrc/binding.cpp (the host compiler, PyTorch's and
+Python's headers) becomes the module that Python calls of k3mx_mx.h go
+through, one file per version of the two.
 """
 import concurrent.futures
 import glob
 import os
 import subprocess
+import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libk3mx.so")
+
+BINDING = os.path.join(HERE, f"_k3mx_binding-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,14 +56,38 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def build_binding(force=False):
+    """Compile csrc/binding.cpp; returns the module's path."""
+    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "k3mx_mx.h")
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (src, header)):
+        return BINDING
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    dirs = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for d in dirs for f in ("-isystem", d)], src, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force=False, verbose_ptxas=False):
-    """Compile every kernel source and link libk3mx.so; returns its path."""
-    if not force and not verbose_ptxas and up_to_date():
-        return LIB
+    """Compile every kernel source and link libk3mx.so, and the binding's
+    module beside it; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(build_binding, force)
+        if not force and not verbose_ptxas and up_to_date():
+            binding.result()
+            return LIB
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     if verbose_ptxas:
         for (_, log), s in zip(results, srcs):
             print(f"== {os.path.basename(s)}\n{log}")
