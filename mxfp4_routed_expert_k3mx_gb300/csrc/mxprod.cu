@@ -43,10 +43,12 @@
 // set-up, one latency, the MMA's, the epilogue), an exchange of a cluster takes
 // one more, and a tile 0.18 us however few rows it has (an MMA of 16 columns
 // costs what one of 96 does), so that HBM is only reached where every SM has
-// many tiles.  Many rows: without its MMAs the kernel takes 183 of 216 us, with
-// half of them 191, with a sixteenth of the rows' copies 204, without stores 200:
-// the copies of 48 KB a tile into shared memory and the MMAs that read it
-// overlap almost wholly, and neither alone is the limit.
+// many tiles.  Many rows: an SM takes a tile's 8 KB of weights and 32 KB of rows
+// from L2 in about 0.33 us (64 bytes a clock), its MMAs take 0.27, and the
+// accumulator changes hands once an item.  Without the MMAs the kernel takes
+// 183 of 216 us, with half of them 191, with a sixteenth of the rows' copies
+// 204, without stores 200.  Units of 192 rows with two accumulators and a
+// fifth stage take 222 (0.28 us a tile, but a third more tiles).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
