@@ -41,9 +41,11 @@
 //   16384 rows of 64 groups, 4096 x 3584     214 us, 2250 TFLOP/s
 // Few rows: about 3 us pass before the first and after the last tile (launch,
 // set-up, one latency, the MMA's, the epilogue), an exchange of a cluster takes
-// one more, and a tile 0.18 us however few rows it has (an MMA of 16 columns
-// costs what one of 96 does), so that HBM is only reached where every SM has
-// many tiles.  Many rows: an SM takes a tile's 8 KB of weights and 32 KB of rows
+// one more, and a tile 0.18 us however few rows it has: the copy writes its
+// 16 KB of spread codes into shared memory and the MMAs read them once, 256 of
+// some 350 clocks (half the MMAs: 13.2 to 11.6 us for 1 x 12288 x 7168; no scale
+// copies: 12.75; weights from L2: 12.5; no scale loads: no change).  HBM is
+// only reached where every SM has many tiles.  Many rows: an SM takes a tile's 8 KB of weights and 32 KB of rows
 // from L2 in about 0.33 us (64 bytes a clock), its MMAs take 0.27, and the
 // accumulator changes hands once an item.  Without the MMAs the kernel takes
 // 183 of 216 us, with half of them 191, with a sixteenth of the rows' copies
