@@ -98,6 +98,7 @@ template <int NT_> struct Shape {
     static constexpr int TMEM_COLS = 512;
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
+    static_assert(SF_COL % 4 == 0 && SF_STEP % 4 == 0, "addresses the MMA reads scales from");
     static_assert(SA * KS >= kGroup, "a group's weight tiles fit the ring (its dropped blocks are zeroed together)");
 };
 
