@@ -20,7 +20,8 @@
 //               loaded some groups ahead into registers, stored as the 32-line
 //               sources of tcgen05.cp, one fence and one barrier per group; a
 //               block of scale 255 gets scale 0 and its codes are zeroed once
-//               the tile landed, so it adds exactly 0
+//               the group before is multiplied and the tile landed, so it
+//               adds exactly 0
 //   warp 2      owns TMEM; one elected lane copies scales to TMEM and issues the
 //               MMAs (the whole warp walks the loop, so that addresses and
 //               descriptors stay in uniform registers: with one lane in the
@@ -99,7 +100,8 @@ template <int NT_> struct Shape {
     static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
     static_assert(SF_COL + SG * kGroup * SF_STEP <= TMEM_COLS, "TMEM");
     static_assert(SF_COL % 4 == 0 && SF_STEP % 4 == 0, "addresses the MMA reads scales from");
-    static_assert(SA * KS >= kGroup, "a group's weight tiles fit the ring (its dropped blocks are zeroed together)");
+    static_assert(SA * KS >= kGroup, "a group's weight tiles fit the ring together: its dropped blocks are zeroed with "
+                                     "the group before consumed and none of its own");
 };
 
 // weights, and the rows in boxes of 16, 32 and 64
@@ -295,11 +297,21 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
 // The blocks of scale 255 of a group of `n` tiles, v[4][kGroup] the scale words
 // of this lane's rows: codes zeroed once each tile has landed, scales too.
 // False if a wait gave up.
+// First the MMAs of the group before are waited for.  The scales' warp runs up
+// to SG groups ahead of them, which is further than the ring is long, and a
+// barrier whose use before the one meant is still open has the parity that is
+// waited for: the zeros went into the slot's earlier tile, where a group with a
+// dropped block followed groups without one.  With the group before consumed,
+// every stage before this group's has landed, the next use of each of its slots
+// is its own, and (the static_assert above) the group's own stages fit the
+// ring; nothing of the group before waits for this one.
 struct DropAt {
+    uint32_t before, parity;            // the barrier of the MMAs of the group before
     uint32_t tfull0, ring, stage;
     int KS, SA, first, c, n;            // the item's first stage, the group's first tile in it
 };
 __device__ __noinline__ bool drop_blocks(const DropAt d, uint32_t *v, int lane) {
+    if (!mbar_wait(d.before, d.parity)) return false;
 #pragma unroll 1
     for (int j = 0; j < kGroup && j < d.n; j++) {
         const int f = d.first + (d.c + j) / d.KS, s = f % d.SA;
@@ -506,7 +518,10 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     nan |= (~v[r][j] - 0x01010101u) & v[r][j] & 0x80808080u;      // a byte of ~v is 0
                 }
             if (__any_sync(0xffffffffu, nan != 0)) {
-                const DropAt at{tfull0, ring, Sh::STAGE, KS, SA, i * fts, c, kcs - c};
+                // (before the first group: the last slot's barrier, free from the start)
+                const int b = n + SG - 1;
+                const DropAt at{gempty0 + 8 * (b % SG), (uint32_t)(((b / SG) & 1) ^ 1), tfull0, ring, Sh::STAGE,
+                                KS,                     SA,                             i * fts, c,  kcs - c};
                 uint32_t u[4 * kGroup];
 #pragma unroll
                 for (int t = 0; t < 4 * kGroup; t++) u[t] = v[t / kGroup][t % kGroup];
