@@ -131,9 +131,13 @@ __device__ __forceinline__ void st_async4(uint32_t addr, float a, float b, float
                  "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
                  : "memory");
 }
+// An exchange's wait.  Its limit is not the one that callers set: after another
+// wait gave up the cluster's CTAs still go through every exchange in step (the
+// parts are worthless and y is not written), so that each barrier is armed once a
+// phase and no part is under way when a CTA leaves.  Twice the limit of the
+// others, which a peer may wait out first.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
-    const uint32_t lim = wait_polls();
-    for (uint32_t i = 0; i < lim; i++) {
+    for (uint32_t i = 0; i < 2 * kWaitLimit; i++) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -452,6 +456,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         report_status(a.status, kStatusWaitTimeout, detail);
         *abort_flag = 1;
     };
+    uint32_t late = 0;                        // exchanges given up (the epilogue's)
 
     if (warp == 0) {
         // ---------------------------------------------------- copies --
@@ -654,8 +659,14 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
         Slot<NBUF> sb;
         Slot<2> ex;
         // `alive` as in the MMA warp: the loops run to their ends, so the named
-        // barrier below always has all its warps
+        // barrier below always has all its warps.  `missed` counts the exchanges
+        // from the first whose own wait gave up.  From then on nothing is sent
+        // (the peers' waits give up in turn), and only the one after it is still
+        // armed: its barrier's phase before was seen complete, a later one's was
+        // not.  Peers may have sent to these two, not to any later one, for which
+        // they would have to have this CTA's parts of the second.
         bool alive = true;
+        uint32_t missed = 0;
 #pragma unroll 1
         for (int k = 0; k < n_items; k++) {
             const Item it = next_item(k);
@@ -731,7 +742,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     const uint32_t buf = smem_addr(red) + ex.i * kExBytes, bar = exfull0 + 8 * ex.i;
                     __syncwarp();
                     named_sync(1, kEpiThreads);
-                    if (warp == kEpi0 && lane == 0) mbar_arrive_expect_tx(bar, S * RS * cols * 16 / 4);
+                    if (warp == kEpi0 && lane == 0 && missed < 2) mbar_arrive_expect_tx(bar, S * RS * cols * 16 / 4);
                     const uint32_t to = map_rank(buf + (rank * RS + o - own * RS) * (kExPitch * 4), own), tobar = map_rank(bar, own);
                     constexpr int PER = HC < kExCols ? HC : kExCols;             // this warp's rows of an exchange
                     if (HC < kExCols || x / (HC / PER) == half) {
@@ -739,10 +750,14 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                         for (int j = 0; j < PER; j += 4) {
                             const int jj = HC < kExCols ? j : (x % (HC / PER)) * PER + j;      // in v
                             const int n = HC < kExCols ? n0 + j : j;                           // of the exchange
-                            if (n < cols) st_async4(to + n * 4, v[jj], v[jj + 1], v[jj + 2], v[jj + 3], tobar);
+                            if (n < cols && missed == 0) st_async4(to + n * 4, v[jj], v[jj + 1], v[jj + 2], v[jj + 3], tobar);
                         }
                     }
-                    alive = alive && wait_cluster(bar, ex.ph);
+                    if (missed != 0 || !wait_cluster(bar, ex.ph)) {
+                        if (missed < 2) late |= (2u | ex.ph) << (2 * ex.i);
+                        missed++;
+                        alive = false;
+                    }
                     __syncwarp();
                     const float *src = reinterpret_cast<const float *>(red + ex.i * kExBytes);
 #pragma unroll 1
@@ -787,9 +802,12 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
     }
     if (S > 1) {
         cluster_sync();                      // no CTA leaves while another may write to its shared memory
-        // a CTA that gave up waiting has not seen all parts land; all are sent by now
-        if (tid == 0 && *abort_flag)
-            for (int i = 0; i < 100; i++) __nanosleep(1000);
+        // nor while parts are under way to it: all are sent by now, and those of
+        // an exchange that was given up (armed by this thread) land first
+        if (tid == kEpi0 * 32)
+            for (int i = 0; i < 2; i++)
+                if ((late >> (2 * i) & 2u) && !mbar_wait_drain(exfull0 + 8 * i, late >> (2 * i) & 1u))
+                    report_status(a.status, kStatusWaitTimeout, 451);
     }
 }
 
