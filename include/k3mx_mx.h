@@ -80,8 +80,9 @@ k3mx_status k3mx_mx_dequantize(void *y, int y_dtype, const uint8_t *codes, const
  *   1 <= n_tokens <= K3MX_MX_MAX_ROWS, width a multiple of 32 up to
  *   K3MX_NORM_MAX_WIDTH.  All pointers 16-byte aligned (scales: any), ldx a
  *   multiple of 16 bytes.
- * |n - exact| <= 2^-20 |exact| for finite rows whose mean square is a normal
- * fp32 number.
+ * |n - exact| <= 2^-20 |exact| for finite rows s whose root mean square lies
+ * in 2^-63 .. 2^120 (squares may leave fp32), where n and the factor
+ * g / sqrt(mean + eps) are normal fp32 numbers.
  */
 k3mx_status k3mx_rmsnorm_mx(uint8_t *codes, uint8_t *scales, void *sum, uint16_t *normed,
                             const void *x, int64_t ldx, const void *residual, int dtype,

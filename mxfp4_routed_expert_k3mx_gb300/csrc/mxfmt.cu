@@ -9,8 +9,8 @@
 // measured copy of 6.77 TB/s):
 //   quantise 12288 x 7168 fp32 to MXFP4    56.9 us, 7.0 TB/s; back 58.7 us, 6.8
 //   quantise 4096 x 7168 bf16 to MXFP8     14.8 us, 6.0 TB/s; back 15.0 us, 5.9
-//   norm 4096 x 7168 fp32, no normed       59.4 us, 6.4 TB/s
-//   norm 4096 x 7168 bf16, with normed     49.0 us, 5.4 TB/s; without 44.6, 4.6
+//   norm 4096 x 7168 fp32, no normed       60.2 us, 6.4 TB/s
+//   norm 4096 x 7168 bf16, with normed     49.6 us, 5.3 TB/s; without 45.2, 4.6
 //   one row of 7168 bf16: quantise 1.3 us, back 1.2, norm 2.9 (launch and one
 //   or two memory latencies)
 // The large fp32 calls are bound by HBM.  The bf16 norm has half the bytes for
@@ -355,25 +355,43 @@ __global__ void __launch_bounds__(WARP ? 128 : V == 1 ? 1024 : V == 2 ? 512 : 10
     // Where many roundings average out (a thread's four parts, a warp's lanes)
     // the sum is plain fp32; where each would be the whole sum's, the low half
     // is kept.
-    float sq[4] = {};
+    float ss, sl;
+    auto sum_squares = [&](float by) {
+        float sq[4] = {};
 #pragma unroll
-    for (int p = 0; p < V; p++)
+        for (int p = 0; p < V; p++)
 #pragma unroll
-        for (int j = 0; j < 8; j++) sq[j & 3] = fmaf(v[p][j], v[p][j], sq[j & 3]);
-    float ss = (sq[0] + sq[1]) + (sq[2] + sq[3]), sl = 0.f;
-    if (WARP) {
-        warp_two_sum(ss, sl, 32);
-    } else {
+            for (int j = 0; j < 8; j++) {
+                const float u = v[p][j] * by;
+                sq[j & 3] = fmaf(u, u, sq[j & 3]);
+            }
+        ss = (sq[0] + sq[1]) + (sq[2] + sq[3]), sl = 0.f;
+        if (WARP) {
+            warp_two_sum(ss, sl, 32);
+        } else {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (lane == 0) part[threadIdx.x >> 5] = ss;
-        __syncthreads();
-        const int nw = blockDim.x >> 5, lanes = nw == 1 ? 1 : 1 << (32 - __clz(nw - 1));
-        ss = (lane & (lanes - 1)) < nw ? part[lane & (lanes - 1)] : 0.f;
-        warp_two_sum(ss, sl, lanes);
-    }
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lane == 0) part[threadIdx.x >> 5] = ss;
+            __syncthreads();
+            const int nw = blockDim.x >> 5, lanes = nw == 1 ? 1 : 1 << (32 - __clz(nw - 1));
+            ss = (lane & (lanes - 1)) < nw ? part[lane & (lanes - 1)] : 0.f;
+            warp_two_sum(ss, sl, lanes);
+        }
+    };
+    sum_squares(1.f);
     float k, kl;
-    norm_factor(ss, sl, a.width, a.eps, k, kl);
+    if (ss + a.eps < INFINITY) {
+        norm_factor(ss, sl, a.width, a.eps, k, kl);
+    } else {                              // (a branch that costs 4096 x 7168 bf16 0.8 us)
+        // The squares' sum leaves fp32 (values from 2^56 on do, in wide rows): it
+        // is formed again of 2^-72 times the values, below 2^128 for any finite
+        // ones, and what is lost at its lower end is below 2^-90 of it.  The
+        // same for every thread of the row.
+        if (!WARP) __syncthreads();                       // part[] has been read
+        sum_squares(0x1p-72f);
+        norm_factor(ss, sl, a.width, a.eps * 0x1p-144f, k, kl);
+        k *= 0x1p-72f, kl *= 0x1p-72f;
+    }
 #pragma unroll
     for (int p = 0; p < V; p++) {
         const int i = p * P + i0;
