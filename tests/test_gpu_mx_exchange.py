@@ -42,7 +42,10 @@ def test_exchanges_after_a_wait_gave_up(cuda_dev, dtype, rows, inner, out, group
     finally:
         k3mx.k3mx_set_wait_limit(0)
     assert all(st == 0 or st == 6 and 400 <= detail < 460 for st, detail in seen), seen
-    assert any(st == 6 for st, _ in seen), "no wait ran out"
+    # a poll lasts up to 2 us: one bf16 accumulation of 64 tiles a CTA is sure to
+    # outlast it, an fp32 one of eight tiles or 32 tiles in all may not
+    if dtype == torch.bfloat16 and inner == 65536:
+        assert any(st == 6 for st, _ in seen), "no wait ran out"
     for _ in range(3):
         y.fill_(0)
         call()
