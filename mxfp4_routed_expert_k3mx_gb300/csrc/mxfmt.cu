@@ -207,7 +207,7 @@ k_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int64_t n8, int pe
 
 template <int FMT, bool BF16, int U>
 __global__ void __launch_bounds__(kFmtThreads)
-k_mx_dequantize(void *y, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t n8) {
+k_mx_dequantize(void *y, const uint8_t *codes, const uint8_t *scales, int64_t n8) {
     pdl_wait();
     pdl_launch_dependents();
     const int64_t i0 = (int64_t)blockIdx.x * (kFmtThreads * U) + threadIdx.x;

@@ -195,12 +195,15 @@ template <int N> struct Slot {
     }
 };
 
-// loads that happen or leave their registers alone (a predicate and no branch)
+// Loads that happen or leave their registers alone (a predicate and no branch).
+// Not through the read-only path, as no load of this kernel's inputs: they may be
+// the kernel's before, which this one overlaps until its dependency wait, and
+// that path is for what nothing writes while a kernel lasts.
 __device__ __forceinline__ void ldg_if(uint32_t &v, const uint8_t *p, bool live) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(p), "r"((uint32_t)live));
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(p), "r"((uint32_t)live));
 }
 __device__ __forceinline__ void ldg2_if(uint32_t &v, uint32_t &w, const uint8_t *p, bool live) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
                  : "+r"(v), "+r"(w) : "l"(p), "r"((uint32_t)live));
 }
 
@@ -224,10 +227,10 @@ __device__ __forceinline__ void scale_groups_w(int n_items, int kcs, Begin begin
         for (int r = 0; r < R; r++) {
             const uint8_t *at = base[r] + 4 * c;
             if (W == 16) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at));
+                const uint4 v = *reinterpret_cast<const uint4 *>(at);
                 q[r][0] = v.x, q[r][1] = v.y, q[r][2] = v.z, q[r][3] = v.w;
             } else if (W == 8) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+                const uint2 v = *reinterpret_cast<const uint2 *>(at);
                 q[r][0] = v.x, q[r][1] = v.y;
                 ldg2_if(q[r][2], q[r][3], at + 8, c + 2 < kcs);
             } else {
@@ -403,7 +406,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             const int g = tid * GPT + k;
             nu[k] = 0;
             if (g < a.n_groups) {
-                const int lo = __ldg(a.offsets + g), hi = __ldg(a.offsets + g + 1);
+                const int lo = a.offsets[g], hi = a.offsets[g + 1];
                 if (lo < 0 || hi < lo || hi > a.n_rows) {
                     if (blockIdx.x == 0) report_status(a.status, kStatusBadIndex, g);
                 } else {
