@@ -486,10 +486,11 @@ def _mx_rows(x, name):
     return rows, cols
 
 
-def _mx_refuse(rows, cols, fmt, shapes, bytes_, values, strided=None):
+def _mx_refuse(rows, cols, fmt, shapes, bytes_, values, strided=None, other=()):
     """Raises for the first argument that is not as expected: format and
     sizes, then shapes, then types and devices.  shapes: (tensor, shape, name);
-    bytes_, values: (tensor, name), values of `strided`'s or their own type."""
+    bytes_, values: (tensor, name), values of `strided`'s or their own type;
+    other: those that the caller has looked at but for their device's number."""
     if fmt not in (K3MX_MXFP4, K3MX_MXFP8):
         raise ValueError(f"fmt: K3MX_MXFP4 or K3MX_MXFP8 expected, got {fmt!r}")
     if rows < 1 or cols < 32 or cols % 32:
@@ -505,6 +506,10 @@ def _mx_refuse(rows, cols, fmt, shapes, bytes_, values, strided=None):
         _dev(t, strided[0].dtype if strided else t.dtype, name)
     if strided and not strided[0].is_cuda:
         raise TypeError(f"{strided[1]}: CUDA tensor expected")
+    current = torch.cuda.current_device()
+    for t, name in [*bytes_, *values, *([strided] if strided else []), *other]:
+        if t.get_device() != current:
+            raise TypeError(f"{name}: a tensor of the current device (cuda:{current}) expected, got one on {t.device}")
     raise TypeError("arguments of unexpected type, device or layout")
 
 
@@ -553,12 +558,13 @@ def k3mx_rmsnorm_mx(codes, scales, sum, x, residual, weight, eps, normed=None, s
             _mx_need(t, shape, n)
         _dev(weight, torch.bfloat16, "weight")
         _dev_opt(normed, torch.bfloat16, "normed")
-        _mx_refuse(rows, cols, K3MX_MXFP8, [], [(codes, "codes"), (scales, "scales")], given, strided=(x, "x"))
+        _mx_refuse(rows, cols, K3MX_MXFP8, [], [(codes, "codes"), (scales, "scales")], given, strided=(x, "x"),
+                   other=[(t, n) for t, n in ((weight, "weight"), (normed, "normed")) if t is not None])
     _check("k3mx_rmsnorm_mx", st)
     return codes, scales
 
 
-def _mx_product_refuse(y, codes, scales, packed, wscales, lead):
+def _mx_product_refuse(y, codes, scales, packed, wscales, lead, other=()):
     """lead: () for the dense product, (groups,) for the grouped one."""
     rows, inner = _mx_rows(codes, "codes")
     if not isinstance(y, torch.Tensor) or y.dim() != 2 or y.shape[0] != rows or y.shape[1] < 1:
@@ -567,7 +573,7 @@ def _mx_product_refuse(y, codes, scales, packed, wscales, lead):
     _mx_refuse(rows, inner, K3MX_MXFP8,
                [(scales, (rows, inner // 32), "scales"), (packed, (*lead, out, inner // 2), "packed"),
                 (wscales, (*lead, out, inner // 32), "wscales")],
-               [(codes, "codes"), (scales, "scales"), (packed, "packed"), (wscales, "wscales")], [(y, "y")])
+               [(codes, "codes"), (scales, "scales"), (packed, "packed"), (wscales, "wscales")], [(y, "y")], other=other)
 
 
 def k3mx_mx_linear(y, codes, scales, packed, wscales, stream=None):
@@ -589,7 +595,7 @@ def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
             raise TypeError("offsets: shape [groups + 1] expected")
         if all(isinstance(t, torch.Tensor) and t.is_cuda for t in (y, codes, scales, packed, wscales)):
             _dev(offsets, torch.int32, "offsets")
-        _mx_product_refuse(y, codes, scales, packed, wscales, (offsets.shape[0] - 1,))
+        _mx_product_refuse(y, codes, scales, packed, wscales, (offsets.shape[0] - 1,), other=[(offsets, "offsets")])
     _check("k3mx_mx_grouped", st)
     return y
 

@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/core/TensorBody.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -32,11 +33,15 @@ struct {
 
 struct Unexpected {};
 
+// the device that this thread's call runs on: the current one, whose stream it
+// takes and whose memory all its tensors have to be in
+thread_local int device;
+
 // (the returned reference is borrowed: the caller's arguments hold it)
 const at::Tensor &cuda_tensor(PyObject *o) {
     if (!THPVariable_Check(o)) throw Unexpected();
     const at::Tensor &t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided || t.is_neg()) throw Unexpected();
+    if (!t.is_cuda() || t.get_device() != device || t.layout() != at::kStrided || t.is_neg()) throw Unexpected();
     return t;
 }
 // contiguous, of a type and a shape; its address
@@ -93,6 +98,7 @@ template <typename F> PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F work) {
     long st = kUnexpected;
     if (n == want) {
         try {
+            device = c10::cuda::current_device();
             auto call = work();
             Py_BEGIN_ALLOW_THREADS
             st = call();
