@@ -448,9 +448,9 @@ _U8 = torch.uint8
 def _load_binding():
     """Puts the module's functions, bound to the library's, in the places of
     the ones below."""
-    path = _build.BINDING
+    path = _build.binding_path()
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+        raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build(), which warns where it cannot")
     spec = importlib.util.spec_from_file_location("_k3mx_binding", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

@@ -4,7 +4,8 @@ Each .cu file compiles to its own object in parallel; the objects link into
 one shared library next to this file.  Rebuilds only when a source or header
 is newer than the library.  csrc/binding.cpp (the host compiler, PyTorch's and
 Python's headers) becomes the module that Python calls of k3mx_mx.h go
-through, one file per version of the two.
+through, one file per version of the two.  The library does not need it: where
+it cannot be compiled, build() warns, and those calls alone raise.
 """
 import concurrent.futures
 import glob
@@ -12,8 +13,7 @@ import os
 import subprocess
 import sys
 import sysconfig
-
-import torch
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,8 +21,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libk3mx.so")
-
-BINDING = os.path.join(HERE, f"_k3mx_binding-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -56,15 +54,24 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def binding_path():
+    import torch
+    return os.path.join(HERE, f"_k3mx_binding-torch{torch.__version__}-{sys.implementation.cache_tag}.so")
+
+
 def build_binding(force=False):
     """Compile csrc/binding.cpp; returns the module's path."""
-    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "k3mx_mx.h")
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in (src, header)):
-        return BINDING
+    import torch
+    src, out = os.path.join(CSRC, "binding.cpp"), binding_path()
+    deps = [src, *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if os.path.exists(out):
+        if not force and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+            return out
+        os.remove(out)              # not an older one's calls, should this one not compile
     base = os.path.dirname(os.path.abspath(torch.__file__))
     dirs = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "/usr/local/cuda/include", sysconfig.get_paths()["include"]]
-    tmp = BINDING + ".tmp"
+    tmp = out + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f for d in dirs for f in ("-isystem", d)], src, "-o", tmp, "-L", os.path.join(base, "lib"),
@@ -72,22 +79,35 @@ def build_binding(force=False):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, out)
+    return out
+
+
+def _binding_or_warning(force):
+    """None, or why there is no binding."""
+    try:
+        build_binding(force)
+    except Exception as e:                      # (no PyTorch, no headers, no compiler, its errors)
+        return f"the Python calls of k3mx_mx.h are not available, their module was not built: {e}"
 
 
 def build(force=False, verbose_ptxas=False):
     """Compile every kernel source and link libk3mx.so, and the binding's
-    module beside it; returns the library's path."""
+    module beside it (a warning if that fails); returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_binding_or_warning, force)
+        if force or verbose_ptxas or not up_to_date():
+            _build_library(verbose_ptxas)
+    if binding.result():
+        warnings.warn(binding.result())
+    return LIB
+
+
+def _build_library(verbose_ptxas):
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
-        binding = ex.submit(build_binding, force)
-        if not force and not verbose_ptxas and up_to_date():
-            binding.result()
-            return LIB
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding.result()
     if verbose_ptxas:
         for (_, log), s in zip(results, srcs):
             print(f"== {os.path.basename(s)}\n{log}")
@@ -99,7 +119,6 @@ def build(force=False, verbose_ptxas=False):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
