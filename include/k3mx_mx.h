@@ -97,8 +97,12 @@ k3mx_status k3mx_rmsnorm_mx(uint8_t *codes, uint8_t *scales, void *sum, uint16_t
  *   1 <= n_tokens, out <= K3MX_MX_MAX_ROWS; in a multiple of 128 up to
  *   K3MX_MX_MAX_IN
  * y, codes 16-byte, packed 32-byte, scales and wscales 4-byte aligned.  The
- * tensor cores multiply the codes exactly and add in fp32: |error| within
- * 1e-5 * sum_c |x w| of the exact sum (before y's rounding).  A weight block
+ * tensor cores multiply the codes exactly and add in fp32 with cut, not
+ * rounded, addends, 1024 columns at a time for K3MX_F32 and 8192 for
+ * K3MX_BF16; these sums are added in fp32.  |error| <= 4e-5 * sum_c |x w| for
+ * K3MX_F32 and 3e-4 * sum_c |x w| for K3MX_BF16 (before y's rounding),
+ * reached where a large term is followed by many that are 2^-26 of it; for
+ * terms of mixed signs and sizes it is below 1e-5.  A weight block
  * of scale 255 adds exactly 0; a NaN code or scale of x makes its whole row
  * of y NaN.  Deterministic.
  */
