@@ -154,14 +154,26 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// 16 TMEM columns of this warp's lanes; the values are there after
-// tmem_ld_wait (which the compiler may not move their uses ahead of)
+// 16 TMEM columns of this warp's lanes; the values are there after tmem_ld_wait
 __device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
           "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr));
+}
+// tmem_ld_wait for the values `v`.  Their uses are register arithmetic, which a
+// wait that does not name them would not hold back: it hands them on.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(float (&v)[N]) {
+    static_assert(N % 16 == 0, "whole loads");
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < N; j += 16)
+        asm volatile(""
+                     : "+f"(v[j]), "+f"(v[j + 1]), "+f"(v[j + 2]), "+f"(v[j + 3]), "+f"(v[j + 4]), "+f"(v[j + 5]),
+                       "+f"(v[j + 6]), "+f"(v[j + 7]), "+f"(v[j + 8]), "+f"(v[j + 9]), "+f"(v[j + 10]), "+f"(v[j + 11]),
+                       "+f"(v[j + 12]), "+f"(v[j + 13]), "+f"(v[j + 14]), "+f"(v[j + 15]));
 }
 // one lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -683,7 +695,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < HC; j += 16) tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, v + j);
-            tmem_ld_wait();
+            tmem_ld_wait_for(v);
             tc_fence_before();
             mbar_arrive(acce0 + 8 * sb.i);
             sb.next();
@@ -697,7 +709,7 @@ k_mx_product(const ProdArgs a, const int y_bf16, const int S, const int seg, con
                     if (n0 + j < n1) {
                         float u[16];
                         tmem_ld16f(tmem + quarter + sb.i * NT + n0 + j, u);
-                        tmem_ld_wait();
+                        tmem_ld_wait_for(u);
 #pragma unroll
                         for (int i = 0; i < 16; i++) v[j + i] += u[i];
                     }
