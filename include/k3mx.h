@@ -366,7 +366,8 @@ k3mx_status k3mx_device_status(k3mx_stream_t stream, int *detail);
  * pipeline barrier, or on a flag another CTA sets) give up after `polls`
  * polls (each at most a few microseconds) and report K3MX_ETIMEOUT through
  * k3mx_device_status; the CTA then waits for its own copies in flight and
- * its MMAs with the default limit, frees its tensor memory and returns, so
+ * its MMAs with the default limit (and goes through the exchanges of its
+ * cluster, with twice that), frees its tensor memory and returns, so
  * the context stays usable and the next call runs normally.  polls = 0
  * restores the default (2^22 polls, seconds); larger values are clamped to
  * it.  Applies to the current device, from the next launch on; outputs of a

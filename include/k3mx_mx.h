@@ -39,12 +39,15 @@ enum { K3MX_MXFP4 = 0, K3MX_MXFP8 = 1 };
 /*
  * x -> codes and scales.  Per block of 32 columns, m = max |x|: the scale is
  * 2^e with the smallest e >= -127 for which m <= top * 2^e (top = 6 for
- * e2m1, 448 for e4m3), so nothing saturates; code = x / 2^e rounded to the
+ * e2m1, 448 for e4m3), so nothing saturates (a quantiser that takes the
+ * exponent of m less that of the top, as the OCP microscaling specification
+ * suggests, gives a smaller scale where m's mantissa is above the top's, and
+ * saturates there); code = x / 2^e rounded to the
  * nearest code value, ties to the even code; byte e + 127.  An all-zero
  * block has byte 0.  A block that holds Inf or NaN gets byte 255 and zero
  * codes; for K3MX_MXFP4, where products skip such a block, that is also
  * reported by k3mx_device_status (K3MX_EINVAL, detail = the row).
- *   x [rows] rows of cols values, ldx elements apart (ldx >= cols), x_dtype
+ *   x [rows] rows of cols values, ldx elements apart (cols <= ldx <= 2^32), x_dtype
  *   K3MX_F32 or K3MX_BF16, aligned to its element; rows whose address and
  *   pitch are multiples of 16 bytes are read with wide loads
  *   codes, scales: written, contiguous, codes 16-byte aligned
@@ -69,7 +72,8 @@ k3mx_status k3mx_mx_dequantize(void *y, int y_dtype, const uint8_t *codes, const
  *   s = x + residual (fp32), n = s * g / sqrt(mean(s^2) + eps) (fp32),
  *   codes, scales = k3mx_mx_quantize of n,
  *   sum = s and normed = n, each rounded to its type once.
- *   x [n_tokens] rows ldx elements apart, dtype K3MX_F32 or K3MX_BF16
+ *   x [n_tokens] rows ldx elements apart (width <= ldx <= 2^32), dtype K3MX_F32
+ *   or K3MX_BF16
  *   residual [n_tokens][width], the same type; NULL: s = x and sum is not
  *   written (pass NULL)
  *   sum [n_tokens][width], x's type, written; may be residual itself, or x
@@ -103,7 +107,9 @@ k3mx_status k3mx_rmsnorm_mx(uint8_t *codes, uint8_t *scales, void *sum, uint16_t
  * K3MX_F32 and 3e-4 * sum_c |x w| for K3MX_BF16 (before y's rounding),
  * reached where a large term is followed by many that are 2^-26 of it; for
  * terms of mixed signs and sizes it is below 1e-5.  A weight block
- * of scale 255 adds exactly 0; a NaN code or scale of x makes its whole row
+ * of scale 255 adds exactly 0 (they are taken to be rare: one in every 128
+ * outputs x 512 columns makes a call three to four times slower); a NaN code
+ * or scale of x makes its whole row
  * of y NaN.  Deterministic.
  */
 k3mx_status k3mx_mx_linear(void *y, int y_dtype, const uint8_t *codes, const uint8_t *scales,

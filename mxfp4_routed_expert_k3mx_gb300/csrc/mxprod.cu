@@ -29,17 +29,20 @@
 //   warp 3      the rows' scales, as warp 1's
 //   warps 4-11  epilogue: two warps to a lane quarter, half the rows each
 // Every wait is bounded; one that gives up is reported on the device status
-// word and every role leaves its loop.
+// word and every role leaves its loop (the epilogue after the exchanges that its
+// cluster still has).
 //
-// Measured (repeated calls; of a measured copy of 6.77 TB/s and library bf16 of
-// 1957 TFLOP/s in a burst):
-//   1 x 3584 x 7168 bf16 (rows, out, in)      7.5 us, 1.8 TB/s of weights and scales
+// Measured (calls repeated in a graph, in a burst; of a measured copy of 6.77 TB/s
+// and library bf16 of 1957 TFLOP/s):
+//   1 x 3584 x 7168 bf16 (rows, out, in)      7.4 us, 1.8 TB/s of weights and scales
 //   1 x 12288 x 7168 bf16                    13.1 us, 3.6 TB/s; 1 x 19456 x 7168 14.4, 5.1
 //   16 rows of 64 groups, 2048 x 3584 bf16   16.2 us, 3.6 TB/s
 //   64 x 12288 x 7168 fp32                   15.9 us, 3.2 TB/s, 710 TFLOP/s
-//   4096 x 12288 x 7168 bf16                 214 us, 3370 TFLOP/s (258 us where the
-//                                            power limit holds the clock near 1.6 GHz)
-//   16384 rows of 64 groups, 4096 x 3584     214 us, 2250 TFLOP/s
+//   4096 x 12288 x 7168 bf16                 213 us, 3390 TFLOP/s; called without pause,
+//                                            where the power limit holds the clock near
+//                                            1.6 GHz, 256 us, 2820
+//   16384 rows of 64 groups, 4096 x 3584     even groups 176 us, 2730 TFLOP/s; uneven ones
+//                                            called without pause 229-235 us, 2050-2100
 // Few rows: about 3 us pass before the first and after the last tile (launch,
 // set-up, one latency, the MMA's, the epilogue), an exchange of a cluster takes
 // one more, and a tile 0.18 us however few rows it has: the copy writes its
