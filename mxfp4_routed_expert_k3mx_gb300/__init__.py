@@ -1,5 +1,5 @@
-"""Python binding of libk3mx.so, the C ABI declared in include/k3mx.h and
-include/k3mx_mx.h.
+"""Python binding of libk3mx.so, the C ABI declared in include/k3mx.h,
+include/k3mx_mx.h and include/k3mx_block.h.
 
 Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  The functions carry the C names; tensors are passed as their
@@ -26,6 +26,7 @@ K3MX_INTER = 3072
 K3MX_EXPERT_BYTES = 17547264
 K3MX_F32, K3MX_BF16 = 0, 1
 K3MX_MXFP4, K3MX_MXFP8 = 0, 1
+K3MX_E4M3 = 2
 K3MX_PATH_AUTO, K3MX_PATH_DECODE, K3MX_PATH_PREFILL, K3MX_PATH_PREFILL_MX = 0, 1, 2, 3
 K3MX_PREFILL_MIN_TOKENS = 256
 K3MX_MAX_TOKENS = 65536
@@ -97,6 +98,15 @@ def lib():
             "k3mx_rmsnorm_mx": ([vp, vp, vp, vp, vp, i64, vp, i, vp, ctypes.c_float, i, i, vp], i),
             "k3mx_mx_linear": ([vp, i, vp, vp, vp, vp, i, i, i, vp], i),
             "k3mx_mx_grouped": ([vp, i, vp, vp, vp, vp, vp, i, i, i, i, vp], i),
+            "k3mx_sort_workspace_size": ([i, i, i], sz),
+            "k3mx_sort": ([vp, vp, vp, vp, i, i, i, vp, sz, vp], i),
+            "k3mx_dispatch": ([vp, vp, vp, vp, i64, i, vp, i, i, i, i, vp], i),
+            "k3mx_combine": ([vp, i, vp, i, vp, vp, vp, i, i, i, i, vp], i),
+            "k3mx_combine_backward": ([vp, vp, vp, i64, i, vp, i, vp, vp, i, i, i, i, vp], i),
+            "k3mx_situ_mx": ([vp, vp, vp, vp, vp, i64, i, i, i, vp], i),
+            "k3mx_situ_mx_backward": ([vp, vp, i64, i, vp, vp, i, i, vp], i),
+            "k3mx_rmsnorm_mx_backward_workspace_size": ([i, i], sz),
+            "k3mx_rmsnorm_mx_backward": ([vp, vp, vp, i64, vp, i, vp, vp, vp, ctypes.c_float, i, i, vp, sz, vp], i),
             "k3mx_trace_enable": ([i], i),
             "k3mx_trace_read": ([ctypes.POINTER(TraceEntry), i], i),
         }
@@ -440,6 +450,8 @@ def k3mx_moe_routed_host(y_host, x_host, experts, logits_host, bias_host, worksp
 # whether the arguments are as they should be and calls the C function; only
 # where they are not, the functions here look for what is wrong and name it.
 
+_BLOCK_FUNCS = ("k3mx_sort", "k3mx_dispatch", "k3mx_combine", "k3mx_combine_backward", "k3mx_situ_mx",
+                "k3mx_situ_mx_backward", "k3mx_rmsnorm_mx_backward")
 _MX_FUNCS = ("k3mx_mx_quantize", "k3mx_mx_dequantize", "k3mx_rmsnorm_mx", "k3mx_mx_linear", "k3mx_mx_grouped")
 _MX_DTYPES = {torch.float32: K3MX_F32, torch.bfloat16: K3MX_BF16}
 _U8 = torch.uint8
@@ -454,8 +466,9 @@ def _load_binding():
     spec = importlib.util.spec_from_file_location("_k3mx_binding", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in _MX_FUNCS))
-    for name in _MX_FUNCS:
+    for bind, names in ((module.bind, _MX_FUNCS), (module.bind_block, _BLOCK_FUNCS)):
+        bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in names))
+    for name in _MX_FUNCS + _BLOCK_FUNCS:
         globals()[name[len("k3mx"):]] = getattr(module, name[len("k3mx_"):])
 
 
@@ -468,6 +481,8 @@ def _entry(name):
 
 
 _mx_quantize, _mx_dequantize, _rmsnorm_mx, _mx_linear, _mx_grouped = (_entry(n[len("k3mx"):]) for n in _MX_FUNCS)
+(_sort, _dispatch, _combine, _combine_backward, _situ_mx, _situ_mx_backward,
+ _rmsnorm_mx_backward) = (_entry(n[len("k3mx"):]) for n in _BLOCK_FUNCS)
 
 
 def _mx_need(t, shape, name):
@@ -598,6 +613,196 @@ def k3mx_mx_grouped(y, codes, scales, packed, wscales, offsets, stream=None):
         _mx_product_refuse(y, codes, scales, packed, wscales, (offsets.shape[0] - 1,), other=[(offsets, "offsets")])
     _check("k3mx_mx_grouped", st)
     return y
+
+
+# ----------------------------------------------- steps of an expert block --
+#
+# As above: the binding asks, and the functions here name what is wrong.
+
+def _block_matrix(t, name, types=(torch.float32, torch.bfloat16), strided=False):
+    """(rows, cols) of a 2-D tensor of one of the types, whole or of rows apart."""
+    rows, cols = _mx_rows(t, name)
+    if t.dtype not in types:
+        raise TypeError(f"{name}: tensor of {' or '.join(str(d).split('.')[-1] for d in types)} expected")
+    if rows < 1 or cols < 1:
+        raise TypeError(f"{name}: at least one row and column expected (shape), got {rows} x {cols}")
+    if not strided and not t.is_contiguous():
+        raise TypeError(f"{name}: contiguous tensor expected")
+    return rows, cols
+
+
+def _block_pairs(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise TypeError(f"{name}: shape [tokens, topk] expected")
+    return tuple(t.shape)
+
+
+def _block_refuse(shapes, ints=(), floats=(), bytes_=(), bf16=(), values=(), workspace=None):
+    """Raises for the first argument that is not as expected: shapes, then
+    types and layouts, then devices.  shapes: (tensor, shape, name); the rest
+    (tensor, name), or for values (tensor, name, type or None where it has been
+    looked at)."""
+    for t, shape, name in shapes:
+        _mx_need(t, shape, name)
+    for given, dtype in ((ints, torch.int32), (floats, torch.float32), (bytes_, _U8), (bf16, torch.bfloat16)):
+        for t, name in given:
+            _dev(t, dtype, name)
+    for t, name, dtype in values:
+        if dtype is not None:
+            _dev(t, dtype, name)
+        if not t.is_cuda:
+            raise TypeError(f"{name}: CUDA tensor expected")
+    if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.is_contiguous()):
+        raise TypeError("workspace: contiguous CUDA tensor expected")
+    current = torch.cuda.current_device()
+    for t, name in [*ints, *floats, *bytes_, *bf16, *((t, n) for t, n, _ in values),
+                    *([(workspace, "workspace")] if workspace is not None else [])]:
+        if t.get_device() != current:
+            raise TypeError(f"{name}: a tensor of the current device (cuda:{current}) expected, got one on {t.device}")
+    raise TypeError("arguments of unexpected type, device or layout")
+
+
+def k3mx_sort_workspace_size(n_tokens, topk, n_experts):
+    return int(lib().k3mx_sort_workspace_size(n_tokens, topk, n_experts))
+
+
+def k3mx_sort(offsets, perm, place, idx, workspace, stream=None):
+    """Pairs of idx [T, topk] (int32, experts 0..E-1 or -1: dropped) by expert,
+    stable: offsets [E + 1], perm (T * topk values or None) the pair of each
+    row, place [T, topk] the row of each pair or -1.  workspace:
+    k3mx_sort_workspace_size bytes (None where that is 0)."""
+    st = _sort(offsets, perm, place, idx, workspace, stream if stream is None else _stream(stream))
+    if st < 0:
+        T, K = _block_pairs(idx, "idx")
+        if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise TypeError("offsets: shape [experts + 1] expected")
+        _numel(perm, T * K, "perm", optional=True)
+        _block_refuse([(place, (T, K), "place")], ints=[(offsets, "offsets"), (place, "place"), (idx, "idx")] +
+                      ([(perm, "perm")] if perm is not None else []), workspace=workspace)
+    _check("k3mx_sort", st)
+    return offsets, perm, place
+
+
+def k3mx_dispatch(rows, x, place, scales=None, x_scales=None, stream=None):
+    """rows[place[t, k]] = x[t], places of -1 skipped: x [T, width] float32,
+    bfloat16 or uint8 (MXFP8 codes; then scales [R, width/32] = x_scales
+    [T, width/32] likewise), rows may be strided; rows [R, width] of the same
+    type.  Rows that no pair names are left as they are."""
+    st = _dispatch(rows, x, place, scales, x_scales, stream if stream is None else _stream(stream))
+    if st < 0:
+        types = (torch.float32, torch.bfloat16, _U8)
+        T, cols = _block_matrix(x, "x", types, strided=True)
+        R, _ = _block_matrix(rows, "rows", types)
+        codes = x.dtype == _U8
+        if codes and cols % 32:
+            raise TypeError(f"x: columns in blocks of 32 expected (shape), got {cols}")
+        K = _block_pairs(place, "place")[1]
+        shapes = [(rows, (R, cols), "rows"), (place, (T, K), "place")]
+        if codes:
+            shapes += [(scales, (R, cols // 32), "scales"), (x_scales, (T, cols // 32), "x_scales")]
+        elif scales is not None or x_scales is not None:
+            raise TypeError("scales, x_scales: None expected (x is not MXFP8 codes)")
+        _block_refuse(shapes, ints=[(place, "place")], bytes_=[(scales, "scales"), (x_scales, "x_scales")] if codes else [],
+                      values=[(x, "x", None), (rows, "rows", x.dtype)])
+    _check("k3mx_dispatch", st)
+    return rows
+
+
+def k3mx_combine(y, rows, place, w=None, base=None, stream=None):
+    """y[t] = base[t] + sum_k w[t, k] rows[place[t, k]], places of -1 skipped:
+    rows [R, width], y and base (optional, may be y) [T, width] of one type,
+    each float32 or bfloat16; w [T, topk] float32, None: all 1."""
+    st = _combine(y, rows, place, w, base, stream if stream is None else _stream(stream))
+    if st < 0:
+        T, cols = _block_matrix(y, "y")
+        R, _ = _block_matrix(rows, "rows")
+        K = _block_pairs(place, "place")[1]
+        shapes = [(rows, (R, cols), "rows"), (place, (T, K), "place")]
+        shapes += [(w, (T, K), "w")] if w is not None else []
+        shapes += [(base, (T, cols), "base")] if base is not None else []
+        _block_refuse(shapes, ints=[(place, "place")], floats=[(w, "w")] if w is not None else [],
+                      values=[(y, "y", None), (rows, "rows", None)] + ([(base, "base", y.dtype)] if base is not None else []))
+    _check("k3mx_combine", st)
+    return y
+
+
+def k3mx_combine_backward(drows, dw, dy, rows, place, w, stream=None):
+    """Gradients of k3mx_combine: drows[place[t, k]] = w[t, k] dy[t] (rows' type;
+    rows that no pair names are left as they are; drows may be rows itself),
+    dw[t, k] = dy[t] . rows[place[t, k]] (float32, 0 where the place is -1).
+    dy [T, width] float32 or bfloat16, rows may be strided."""
+    st = _combine_backward(drows, dw, dy, rows, place, w, stream if stream is None else _stream(stream))
+    if st < 0:
+        T, cols = _block_matrix(dy, "dy", strided=True)
+        R, _ = _block_matrix(rows, "rows")
+        K = _block_pairs(place, "place")[1]
+        _block_refuse([(rows, (R, cols), "rows"), (drows, (R, cols), "drows"), (place, (T, K), "place"), (w, (T, K), "w"),
+                       (dw, (T, K), "dw")], ints=[(place, "place")], floats=[(w, "w"), (dw, "dw")],
+                      values=[(dy, "dy", None), (rows, "rows", None), (drows, "drows", rows.dtype)])
+    _check("k3mx_combine_backward", st)
+    return drows, dw
+
+
+def k3mx_situ_mx(codes, scales, gu, saved=None, saved_scales=None, stream=None):
+    """codes, scales = h in K3MX_MXFP8, h = 4 tanh(g/4) sigma(g) 25 tanh(u/25) of
+    gu = g | u [R, 2 inter] (float32 or bfloat16, rows may be strided); saved,
+    saved_scales (optional) = gu in K3MX_MXFP8 for k3mx_situ_mx_backward."""
+    st = _situ_mx(codes, scales, gu, saved, saved_scales, stream if stream is None else _stream(stream))
+    if st < 0:
+        R, cols = _block_matrix(gu, "gu", strided=True)
+        if cols % 64:
+            raise TypeError(f"gu: two halves in blocks of 32 columns expected (shape), got {cols}")
+        if (saved is None) != (saved_scales is None):
+            raise TypeError("saved_scales: expected exactly where saved is given (shape [R, 2 inter / 32])")
+        shapes = [(codes, (R, cols // 2), "codes"), (scales, (R, cols // 64), "scales")]
+        shapes += [(saved, (R, cols), "saved"), (saved_scales, (R, cols // 32), "saved_scales")] if saved is not None else []
+        _block_refuse(shapes, bytes_=[(t, n) for t, _, n in shapes], values=[(gu, "gu", None)])
+    _check("k3mx_situ_mx", st)
+    return codes, scales
+
+
+def k3mx_situ_mx_backward(dgu, dh, saved, saved_scales, stream=None):
+    """dgu = dg | du [R, 2 inter], the gradient of k3mx_situ_mx at what it saved,
+    from dh [R, inter] of the same type (float32 or bfloat16, rows may be strided)."""
+    st = _situ_mx_backward(dgu, dh, saved, saved_scales, stream if stream is None else _stream(stream))
+    if st < 0:
+        R, cols = _block_matrix(dh, "dh", strided=True)
+        if cols % 32:
+            raise TypeError(f"dh: columns in blocks of 32 expected (shape), got {cols}")
+        _block_refuse([(dgu, (R, 2 * cols), "dgu"), (saved, (R, 2 * cols), "saved"),
+                       (saved_scales, (R, cols // 16), "saved_scales")],
+                      bytes_=[(saved, "saved"), (saved_scales, "saved_scales")],
+                      values=[(dh, "dh", None), (dgu, "dgu", dh.dtype)])
+    _check("k3mx_situ_mx_backward", st)
+    return dgu
+
+
+def k3mx_rmsnorm_mx_backward_workspace_size(n_tokens, width):
+    return int(lib().k3mx_rmsnorm_mx_backward_workspace_size(n_tokens, width))
+
+
+def k3mx_rmsnorm_mx_backward(dx, dweight, dn, saved, saved_scales, weight, eps, workspace, dres=None, stream=None):
+    """The gradient of k3mx_rmsnorm_mx's norm at the sum that saved, saved_scales
+    (K3MX_MXFP8 [T, width]) hold: dx = dres + k (weight dn - n mean(weight dn n)),
+    dweight = sum_t dn n, n = sum k, k = 1 / sqrt(mean(sum^2) + eps).  dn
+    [T, width] float32 or bfloat16 (rows may be strided), dx and dres (optional,
+    may be dx) of its type, dweight float32, weight bfloat16 [width]."""
+    st = _rmsnorm_mx_backward(dx, dweight, dn, saved, saved_scales, weight, eps, workspace, dres,
+                              stream if stream is None else _stream(stream))
+    if st < 0:
+        T, cols = _block_matrix(dn, "dn", strided=True)
+        if cols % 32:
+            raise TypeError(f"dn: columns in blocks of 32 expected (shape), got {cols}")
+        float(eps)
+        _block_refuse([(dx, (T, cols), "dx"), (dweight, (cols,), "dweight"), (saved, (T, cols), "saved"),
+                       (saved_scales, (T, cols // 32), "saved_scales"), (weight, (cols,), "weight")] +
+                      ([(dres, (T, cols), "dres")] if dres is not None else []),
+                      floats=[(dweight, "dweight")], bytes_=[(saved, "saved"), (saved_scales, "saved_scales")],
+                      bf16=[(weight, "weight")],
+                      values=[(dn, "dn", None), (dx, "dx", dn.dtype)] + ([(dres, "dres", dn.dtype)] if dres is not None else []),
+                      workspace=workspace)
+    _check("k3mx_rmsnorm_mx_backward", st)
+    return dx, dweight
 
 
 def k3mx_device_status(stream=None):

@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "blockops.cuh"
 #include "common.cuh"
 #include "dense.cuh"
 #include "mxops.cuh"
@@ -413,6 +414,22 @@ k3mx_status run_mx_product(ProdArgs a, int y_dtype, k3mx_stream_t stream, const 
     if (st != K3MX_OK) return st;
     a.status = c.status;
     return from_cuda(traced(name, c.stream, [&] { return launch_mx_product(c, a, y_dtype == K3MX_BF16); }));
+}
+
+// ------------------------------------------- steps of an expert block --
+
+bool value_type(int dtype) { return dtype == K3MX_F32 || dtype == K3MX_BF16; }
+// aligned to its elements of `n` bytes
+bool aligned_to(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
+int value_bytes(int dtype) { return dtype == K3MX_BF16 ? 2 : dtype == K3MX_F32 ? 4 : 1; }
+
+bool pairs_ok(int n_tokens, int topk) {
+    return n_tokens >= 1 && topk >= 1 && (int64_t)n_tokens * topk <= K3MX_BLOCK_MAX_PAIRS;
+}
+bool block_shape_ok(int n_tokens, int topk, int n_rows, int width, int64_t ld) {
+    return pairs_ok(n_tokens, topk) && n_rows >= 1 && n_rows <= K3MX_MX_MAX_ROWS && width >= 1 &&
+           width <= K3MX_MX_MAX_COLS && (int64_t)n_rows * width <= K3MX_BLOCK_MAX_ELEMENTS &&
+           (int64_t)n_tokens * width <= K3MX_BLOCK_MAX_ELEMENTS && ld >= width && ld <= kMxMaxPitch;
 }
 
 }  // namespace
@@ -878,6 +895,125 @@ k3mx_status k3mx_mx_grouped(void *y, int y_dtype, const uint8_t *codes, const ui
     if (!offsets) return K3MX_EINVAL;
     const ProdArgs a{y, codes, scales, packed, wscales, offsets, n_groups, n_rows, in, out, nullptr};
     return run_mx_product(a, y_dtype, stream, "mx_grouped");
+}
+
+// ------------------------------- steps of an expert block (k3mx_block.h) --
+
+size_t k3mx_sort_workspace_size(int n_tokens, int topk, int n_experts) {
+    if (!pairs_ok(n_tokens, topk) || n_experts < 1 || n_experts > K3MX_MX_MAX_GROUPS) return 0;
+    return up256(sort_scratch_bytes(n_tokens * topk, n_experts));
+}
+
+k3mx_status k3mx_sort(int32_t *offsets, int32_t *perm, int32_t *place, const int32_t *idx, int n_tokens, int topk,
+                      int n_experts, void *workspace, size_t ws_bytes, k3mx_stream_t stream) {
+    if (!offsets || !place || !idx) return K3MX_EINVAL;
+    if (!pairs_ok(n_tokens, topk) || n_experts < 1 || n_experts > K3MX_MX_MAX_GROUPS) return K3MX_ESHAPE;
+    if (!aligned_to(offsets, 4) || !aligned_to(perm, 4) || !aligned_to(place, 4) || !aligned_to(idx, 4)) return K3MX_EALIGN;
+    const size_t need = k3mx_sort_workspace_size(n_tokens, topk, n_experts);
+    if (need > 0 && (!workspace || ws_bytes < need)) return K3MX_EWORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    return from_cuda(traced("sort", c.stream, [&] {
+        return launch_sort(c, offsets, perm, place, idx, n_tokens * topk, n_experts, workspace);
+    }));
+}
+
+k3mx_status k3mx_dispatch(void *rows, uint8_t *scales, const void *x, const uint8_t *x_scales, int64_t ldx, int dtype,
+                          const int32_t *place, int n_tokens, int topk, int n_rows, int width, k3mx_stream_t stream) {
+    if (!rows || !x || !place || (!value_type(dtype) && dtype != K3MX_E4M3)) return K3MX_EINVAL;
+    if ((dtype == K3MX_E4M3) != (scales != nullptr) || (scales != nullptr) != (x_scales != nullptr)) return K3MX_EINVAL;
+    if (!block_shape_ok(n_tokens, topk, n_rows, width, ldx) || (dtype == K3MX_E4M3 && width % 32 != 0)) return K3MX_ESHAPE;
+    const int elem = value_bytes(dtype);
+    if (!aligned_to(rows, elem) || !aligned_to(x, elem) || !aligned_to(place, 4)) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const DispatchArgs a{rows, scales, x, x_scales, ldx, elem, place, n_tokens, topk, n_rows, width, c.status};
+    return from_cuda(traced("dispatch", c.stream, [&] { return launch_dispatch(c, a); }));
+}
+
+k3mx_status k3mx_combine(void *y, int y_dtype, const void *rows, int rows_dtype, const int32_t *place, const float *w,
+                         const void *base, int n_tokens, int topk, int n_rows, int width, k3mx_stream_t stream) {
+    if (!y || !rows || !place || !value_type(y_dtype) || !value_type(rows_dtype)) return K3MX_EINVAL;
+    if (!block_shape_ok(n_tokens, topk, n_rows, width, width)) return K3MX_ESHAPE;
+    if (!aligned_to(y, value_bytes(y_dtype)) || !aligned_to(base, value_bytes(y_dtype)) ||
+        !aligned_to(rows, value_bytes(rows_dtype)) || !aligned_to(place, 4) || !aligned_to(w, 4))
+        return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const CombineArgs a{y, rows, place, w, base, n_tokens, topk, n_rows, width, c.status};
+    return from_cuda(traced("combine", c.stream, [&] {
+        return launch_combine(c, a, y_dtype == K3MX_BF16, rows_dtype == K3MX_BF16);
+    }));
+}
+
+k3mx_status k3mx_combine_backward(void *drows, float *dw, const void *dy, int64_t lddy, int dy_dtype, const void *rows,
+                                  int rows_dtype, const int32_t *place, const float *w, int n_tokens, int topk,
+                                  int n_rows, int width, k3mx_stream_t stream) {
+    if (!drows || !dw || !dy || !rows || !place || !w || !value_type(dy_dtype) || !value_type(rows_dtype)) return K3MX_EINVAL;
+    if (!block_shape_ok(n_tokens, topk, n_rows, width, lddy)) return K3MX_ESHAPE;
+    if (!aligned_to(dy, value_bytes(dy_dtype)) || !aligned_to(rows, value_bytes(rows_dtype)) ||
+        !aligned_to(drows, value_bytes(rows_dtype)) || !aligned_to(dw, 4) || !aligned_to(place, 4) || !aligned_to(w, 4))
+        return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const CombineGradArgs a{drows, dw, dy, lddy, rows, place, w, n_tokens, topk, n_rows, width, c.status};
+    return from_cuda(traced("combine_backward", c.stream, [&] {
+        return launch_combine_grad(c, a, dy_dtype == K3MX_BF16, rows_dtype == K3MX_BF16);
+    }));
+}
+
+k3mx_status k3mx_situ_mx(uint8_t *codes, uint8_t *scales, uint8_t *saved, uint8_t *saved_scales, const void *gu,
+                         int64_t ldgu, int dtype, int rows, int inter, k3mx_stream_t stream) {
+    if (!codes || !scales || !gu || !value_type(dtype) || (saved != nullptr) != (saved_scales != nullptr)) return K3MX_EINVAL;
+    if (!mx_shape_ok(rows, inter) || inter > K3MX_MX_MAX_COLS / 2 || ldgu < 2 * inter || ldgu > kMxMaxPitch) return K3MX_ESHAPE;
+    if (!aligned16(codes) || !aligned16(saved) || !aligned16(gu) || ldgu * value_bytes(dtype) % 16 != 0) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const SituArgs a{codes, scales, saved, saved_scales, gu, ldgu, rows, inter};
+    return from_cuda(traced("situ_mx", c.stream, [&] { return launch_situ(c, a, dtype == K3MX_BF16); }));
+}
+
+k3mx_status k3mx_situ_mx_backward(void *dgu, const void *dh, int64_t lddh, int dtype, const uint8_t *saved,
+                                  const uint8_t *saved_scales, int rows, int inter, k3mx_stream_t stream) {
+    if (!dgu || !dh || !saved || !saved_scales || !value_type(dtype)) return K3MX_EINVAL;
+    if (!mx_shape_ok(rows, inter) || inter > K3MX_MX_MAX_COLS / 2 || lddh < inter || lddh > kMxMaxPitch) return K3MX_ESHAPE;
+    if (!aligned16(dgu) || !aligned16(dh) || !aligned16(saved) || lddh * value_bytes(dtype) % 16 != 0) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const SituGradArgs a{dgu, dh, lddh, saved, saved_scales, rows, inter};
+    return from_cuda(traced("situ_mx_backward", c.stream, [&] { return launch_situ_grad(c, a, dtype == K3MX_BF16); }));
+}
+
+size_t k3mx_rmsnorm_mx_backward_workspace_size(int n_tokens, int width) {
+    if (!mx_shape_ok(n_tokens, width) || width > K3MX_NORM_MAX_WIDTH) return 0;
+    return up256(norm_grad_scratch_bytes(n_tokens, width));
+}
+
+k3mx_status k3mx_rmsnorm_mx_backward(void *dx, float *dweight, const void *dn, int64_t lddn, const void *dres, int dtype,
+                                     const uint8_t *saved, const uint8_t *saved_scales, const uint16_t *g, float eps,
+                                     int n_tokens, int width, void *workspace, size_t ws_bytes, k3mx_stream_t stream) {
+    if (!dx || !dweight || !dn || !saved || !saved_scales || !g || !value_type(dtype)) return K3MX_EINVAL;
+    if (!(eps >= 0.f) || eps == INFINITY) return K3MX_EINVAL;
+    if (!mx_shape_ok(n_tokens, width) || width > K3MX_NORM_MAX_WIDTH || lddn < width || lddn > kMxMaxPitch)
+        return K3MX_ESHAPE;
+    if (!aligned16(dx) || !aligned16(dweight) || !aligned16(dn) || !aligned16(dres) || !aligned16(saved) || !aligned16(g) ||
+        lddn * value_bytes(dtype) % 16 != 0)
+        return K3MX_EALIGN;
+    if (!workspace || ws_bytes < k3mx_rmsnorm_mx_backward_workspace_size(n_tokens, width)) return K3MX_EWORKSPACE;
+    if (!aligned16(workspace)) return K3MX_EALIGN;
+    Ctx c;
+    const k3mx_status st = device_ctx(reinterpret_cast<cudaStream_t>(stream), c);
+    if (st != K3MX_OK) return st;
+    const NormGradArgs a{dx,   dweight,      static_cast<float *>(workspace), dn,  lddn,     dres,
+                         saved, saved_scales, g,                               eps, n_tokens, width};
+    return from_cuda(traced("rmsnorm_mx_backward", c.stream, [&] { return launch_norm_grad(c, a, dtype == K3MX_BF16); }));
 }
 
 k3mx_status k3mx_trace_enable(int on) {
