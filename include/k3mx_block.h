@@ -112,10 +112,12 @@ k3mx_status k3mx_combine_backward(void *drows, float *dw, const void *dy, int64_
  *   1 <= rows <= K3MX_MX_MAX_ROWS, inter a multiple of 32, 2 inter <=
  *   K3MX_MX_MAX_COLS.  Pointers 16-byte aligned (scales: any), ldgu a multiple
  *   of 16 bytes.
- * What is saved is exactly k3mx_mx_quantize's.  h is formed in fp32 within
- * 2^-18 (1 + (|g| + |u|)/16) of itself (where it is a normal fp32 number) and then
- * quantised as k3mx_mx_quantize does.  Infinite g and u have their limits; a
- * NaN makes its block NaN.
+ * What is saved is exactly k3mx_mx_quantize's.  The codes and scales of h are
+ * those that k3mx_mx_quantize's definition gives for h itself, formed within
+ * 2^-29; but a code below 2^-6 (a value under 2^-15 of its block's largest), and
+ * any where g < -16, is that of a value within 2^-15 of h, and where g < -87
+ * h may be taken for 0.  Infinite g and u have their limits; a NaN makes its
+ * block NaN.
  */
 k3mx_status k3mx_situ_mx(uint8_t *codes, uint8_t *scales, uint8_t *saved, uint8_t *saved_scales,
                          const void *gu, int64_t ldgu, int dtype, int rows, int inter, k3mx_stream_t stream);
@@ -127,8 +129,9 @@ k3mx_status k3mx_situ_mx(uint8_t *codes, uint8_t *scales, uint8_t *saved, uint8_
  *       K3MX_BF16
  *   dgu [rows][2 inter] of the same type, written: dg | du
  *   sizes and alignment as for k3mx_situ_mx
- * A saved block of scale 255 (it held Inf or NaN) makes its columns' dg and du
- * NaN.
+ * The derivatives are within 2^-18 (1 + (|g| + |u|)/16) of themselves (dh/dg:
+ * of its two terms' magnitudes) and within 2^-119.  A saved block of scale 255
+ * (it held Inf or NaN) makes its columns' dg and du NaN.
  */
 k3mx_status k3mx_situ_mx_backward(void *dgu, const void *dh, int64_t lddh, int dtype, const uint8_t *saved,
                                   const uint8_t *saved_scales, int rows, int inter, k3mx_stream_t stream);

@@ -35,7 +35,7 @@ def situ(gu, save):
 
 
 def off_of_h(g, u):
-    """What the fp32 value of h may be off by, relative (the header's bound)."""
+    """What the gradients' factors may be off by, relative."""
     return 2.0 ** -18 * (1 + (np.abs(g) + np.abs(u)) / 16)
 
 
@@ -55,19 +55,16 @@ def test_situ(cuda_dev, R, F, kind, pad):
     code, s = mx_ref.quantize(x, mx_ref.MXFP8)
     assert np.array_equal(saved.cpu().numpy(), code) and np.array_equal(ss.cpu().numpy(), s)
     g, u = x[:, :F], x[:, F:]
-    h, off = block_ref.situ(g, u), off_of_h(g, u)
-    m = np.abs(h).reshape(R, F // 32, 32)
-    lo, hi = ((m * (1 + q * off.reshape(m.shape))).max(-1) for q in (-1, 1))
-    s = scales.cpu().numpy().astype(np.int64)
-    pick = lambda m: np.where(m > 0, mx_ref.scale_exponent(np.where(m > 0, m, 1.0), mx_ref.MXFP8), -127) + 127
-    assert np.all((s == pick(lo)) | (s == pick(hi)))
-    # half a code's step (2^-4 of it, or half the smallest code), and what h was off by
+    h = block_ref.situ(g, u)
+    # h's own codes, but for the smallest (values near a middle are formed within 2^-29: one in 30 million may still turn)
+    want, s = mx_ref.quantize(h, mx_ref.MXFP8)
+    got = codes.cpu().numpy()
+    assert np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(np.where(want & 127 >= 8, want, 0), np.where(got & 127 >= 8, got, 0))
+    # those: half a step of 2^-9, and the 2^-15 that h is off by there (64 + 1.5 * 87 units of 2^-24 and as much of bias: 2^-15.4)
     e = np.exp2(s.astype(np.float64) - 127).repeat(32, 1).reshape(R, F)
-    got = mx_ref.values(codes.cpu().numpy(), scales.cpu().numpy(), mx_ref.MXFP8)
-    near = np.abs(h) * (1 + off)
-    assert np.all(np.abs(got - h) <= np.maximum(2.0 ** -4 * near, 2.0 ** -10 * e) + off * np.abs(h))
-    want = mx_ref.quantize(h, mx_ref.MXFP8)[0]
-    assert np.mean(codes.cpu().numpy() != want) <= 2.0 ** -9 + 2.0 / h.size    # (off is 2^-12 of a code's step for most)
+    off = np.abs(mx_ref.values(got, s, mx_ref.MXFP8) - h)
+    assert np.all((off <= 2.0 ** -10 * e + 2.0 ** -15 * np.abs(h)) | (want & 127 >= 8))
     alone = situ(gu, False)
     assert torch.equal(alone[0], codes) and torch.equal(alone[1], scales)
     assert k3mx.k3mx_device_status() == (0, 0)
@@ -148,6 +145,40 @@ def test_situ_backward_is_situs_difference(cuda_dev):
     # differences are off by d^2 / 6 of a third derivative (below 20), and by 2^-52 of h over d; the kernel by 2^-17 of two terms
     tol = 20 * d * d + 2.0 ** -52 * 100 / d
     assert np.all(np.abs(doubles(dgu) - np.concatenate([dg, du], 1)) <= tol + 2.0 ** -17 * 60)
+
+
+@pytest.mark.parametrize("kind", sorted(TYPES))
+def test_situ_backward_of_many_rows(cuda_dev, kind):
+    """Every code under every scale, in calls of many rows and of few: the same bits, and the definition's."""
+    r = np.random.default_rng(2)
+    R, F = 8300, 512
+    code = r.integers(0, 256, size=(R, 2 * F)).astype(np.uint8)
+    s = r.integers(90, 140, size=(R, 2 * F // 32)).astype(np.uint8)
+    s[:64] = r.integers(112, 127, size=(64, 2 * F // 32))
+    s[64:320] = np.arange(256)[:, None]
+    code[64:320] &= 0xBF                                # (smaller values: no infinity below scale 254)
+    dh = rows_of(r.normal(size=(R, F)), kind, 8)
+    dev = lambda t: torch.from_numpy(t).to(DEV)
+    dgu = torch.full((R, 2 * F), 99.0, dtype=TYPES[kind], device=DEV)
+    k3mx.k3mx_situ_mx_backward(dgu, dh, dev(code), dev(s))
+    for at in (slice(0, 64), slice(64, 320), slice(8000, 8300)):
+        few = torch.empty(at.stop - at.start, 2 * F, dtype=TYPES[kind], device=DEV)
+        k3mx.k3mx_situ_mx_backward(few, dh[at], dev(code[at]), dev(s[at]))
+        assert torch.equal(few.nan_to_num(12345.0, 1e38, -1e38), dgu[at].nan_to_num(12345.0, 1e38, -1e38))
+    v = mx_ref.values(code, s, mx_ref.MXFP8)
+    bad = np.isnan(v[:, :F]) | np.isnan(v[:, F:])
+    got = doubles(dgu)
+    assert np.all(np.isnan(got[:, :F]) == bad) and np.all(np.isnan(got[:, F:]) == bad)
+    big = (np.abs(v) > 1e30)[:, :F] | (np.abs(v) > 1e30)[:, F:]
+    v = np.where(np.isnan(v) | (np.abs(v) > 1e30), 0.0, v)
+    g, u = v[:, :F], v[:, F:]
+    dg, du, mag = block_ref.situ_backward(g, u, doubles(dh))
+    off = off_of_h(g, u)
+    for have, want, m in ((got[:, :F], dg, mag), (got[:, F:], du, np.abs(du))):
+        # exponentials below 2^-126 are taken for 0: 4 * 25 of them, below 2^7, are dg's and du's
+        tol = off * m + 2.0 ** -119 * np.abs(doubles(dh))
+        tol += block_ref.HALF[kind] * (np.abs(want) + tol) + 2.0 ** -120
+        assert np.all((np.abs(have - want) <= tol) | bad | big)
 
 
 # --------------------------------------------------------------- the norm --
