@@ -426,86 +426,205 @@ __global__ void __launch_bounds__(kTableThreads, 2) k_situ_grad_table(const Situ
 // (or a warp, for narrow rows) keeps its columns of the weight and of its rows'
 // sum of dn n in registers and walks the rows part by part; the parts are
 // added by a second kernel in their order.
+//
+// A thread has the same runs of every row, so what it needs of the next rows it
+// copies ahead into shared memory for itself (cp.async, D rows deep, no
+// barrier).  D = 0: they come from global memory, for a CTA's only row (64 rows
+// of 7168 fp32: 5.5 us, by way of shared memory 6.5) and for rows that shared
+// memory does not hold: those are read before the sums and from L2 once more
+// after them (KEEP false), and the sums of dn n have the shared memory.
 
-constexpr int kNormParts = 608;       // parts at most, but for the next line
+constexpr int kNormSms = 152;         // parts are a multiple of it (a constant: results do not depend on the device)
 constexpr int kRowsOfPart = 1024;     // rows that one thread adds, at most
+constexpr int kNormSmem = 220 << 10;
 
 struct NormShape {
     bool warp;         // a row to a warp, eight a CTA
+    bool few;          // one row a CTA
     int v, threads, parts;
 };
 NormShape norm_shape(int n_tokens, int width) {
     const int runs = width / 8;
     NormShape s;
     s.warp = runs <= 128;
-    s.v = s.warp ? (runs <= 32 ? 1 : 4) : runs <= 1024 ? 1 : runs <= 2048 ? 2 : 4;
+    s.few = !s.warp && runs <= 1024 && n_tokens <= kNormSms;
+    s.v = s.warp ? (runs <= 32 ? 1 : runs <= 64 ? 2 : 4) : s.few ? 1 : runs <= 2048 ? 2 : 4;
     s.threads = s.warp ? kThreads : (runs + 32 * s.v - 1) / (32 * s.v) * 32;
     const int at_once = s.warp ? kThreads / 32 : 1, full = (n_tokens + at_once - 1) / at_once;
     const int least = (full + kRowsOfPart - 1) / kRowsOfPart;
-    s.parts = full < kNormParts ? full : least > kNormParts ? least : kNormParts;
+    const int most = kNormSms * (s.warp ? 1 : s.threads <= 128 ? 4 : s.threads <= 256 ? 2 : 1);
+    s.parts = full < most ? full : least > most ? least : most;
     return s;
 }
+// bytes that a thread keeps of a run: dn, dres, codes
+constexpr int run_bytes(bool bf16) { return 8 + 2 * (bf16 ? 16 : 32); }
 
-template <bool WARP, int V, bool BF16>
-__global__ void __launch_bounds__(WARP ? kThreads : 1024) k_norm_grad(const NormGradArgs a) {
-    __shared__ float2 sums[2][32];
-    __shared__ float cols[WARP ? kThreads / 32 * 256 * V : 1];
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The sums of a and b over a warp, to all its lanes: one half of it adds a, the
+// other b.
+__device__ __forceinline__ float half_sums(float a, float b) {
+    const bool high = threadIdx.x & 16;
+    float v = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float2 pair(const float (&v)[8], int j) { return make_float2(v[j], v[j + 1]); }
+__device__ __forceinline__ void put(float (&v)[8], int j, float2 f) { v[j] = f.x, v[j + 1] = f.y; }
+
+template <bool WARP, int V, bool BF16, int D, bool KEEP>
+__global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_grad(const NormGradArgs a) {
+    extern __shared__ __align__(16) uint8_t ring[];       // D > 0: [D][V] of dn, dres, codes of the CTA's threads; !KEEP: the sums
+    __shared__ float sums[2][2][32];
+    constexpr int kQ = BF16 ? 1 : 2, kElem = BF16 ? 2 : 4;        // kQ: 16 bytes of a run's dn
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = WARP ? 32 : blockDim.x;
     const int i0 = WARP ? lane : threadIdx.x, runs = a.width / 8;
     const int step = gridDim.x * (WARP ? kThreads / 32 : 1);
-    uint4 gq[V];
-    float acc[V][8] = {};
+    int t = WARP ? blockIdx.x * (kThreads / 32) + warp : blockIdx.x;
+    const int P16 = blockDim.x * 16, slot = (int)blockDim.x * run_bytes(BF16), me = threadIdx.x * 16;
+    // run p of a row: whether it is there; the rest of the row is at 8 P columns' distance
+    auto there = [&](int p) { return p * P + i0 < runs; };
+    const bool res = a.dres != nullptr;
+
+    // the row to be copied ahead
+    int ahead = t;
+    const int64_t first = (int64_t)t * a.width + 8 * i0, pitch = (int64_t)step * a.width, dn_pitch = (int64_t)step * a.lddn * kElem;
+    const uint8_t *from_dn = static_cast<const uint8_t *>(a.dn) + (t * a.lddn + 8 * i0) * kElem;
+    const uint8_t *from_res = static_cast<const uint8_t *>(a.dres) + first * kElem;
+    const uint8_t *from_codes = a.saved + first;
+    auto fetch = [&](uint32_t to) {
+        if (ahead < a.n_tokens) {
 #pragma unroll
-    for (int p = 0; p < V; p++)
-        gq[p] = p * P + i0 < runs ? reinterpret_cast<const uint4 *>(a.g)[p * P + i0] : make_uint4(0u, 0u, 0u, 0u);
-    int flip = 0;
-    for (int64_t t = WARP ? blockIdx.x * (kThreads / 32) + warp : blockIdx.x; t < a.n_tokens; t += step) {
-        float x[V][8], d[V][8];
+            for (int p = 0; p < V; p++)
+                if (there(p)) {
+                    const uint32_t at = to + p * slot;
 #pragma unroll
-        for (int p = 0; p < V; p++) {
-            const int c = p * P + i0;
+                    for (int q = 0; q < kQ; q++) copy16(at + me + q * P16, from_dn + 8 * p * P * kElem + 16 * q);
+                    if (res) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) x[p][j] = d[p][j] = 0.f;
-            if (c < runs) {
-                const int64_t i = t * runs + c;
-                from_e4m3x8(reinterpret_cast<const uint2 *>(a.saved)[i], up_scale(a.saved_scales[i >> 2]), x[p]);
-                load8<BF16, true>(a.dn, t * a.lddn + 8 * c, d[p]);
-            }
+                        for (int q = 0; q < kQ; q++) copy16(at + me + (kQ + q) * P16, from_res + 8 * p * P * kElem + 16 * q);
+                    }
+                    copy8(at + me / 2 + 2 * kQ * P16, from_codes + 8 * p * P);
+                }
+            ahead += step;
+            from_dn += dn_pitch, from_res += pitch * kElem, from_codes += pitch;
         }
+        copies_end_group();
+    };
+    const uint32_t base = D > 0 ? smem_addr(ring) : 0u;
+    if (D > 0) {
+#pragma unroll
+        for (int d = 0; d < D; d++) fetch(base + d * V * slot);
+    }
+    const uint8_t *from_scales = a.saved_scales + (first >> 5);
+    auto scales = [&](int t, uint32_t (&s)[V]) {
+#pragma unroll
+        for (int p = 0; p < V; p++) s[p] = there(p) && t < a.n_tokens ? from_scales[p * P / 4] : 0u;
+        from_scales += pitch >> 5;
+    };
+    uint32_t scale[V];
+    scales(t, scale);
+    uint8_t *to_dx = static_cast<uint8_t *>(a.dx) + first * kElem;
+    float weight[KEEP ? V : 1][8], acc[KEEP ? V : 1][8];
+    auto load_weight = [&](int p, float (&g)[8]) {
+        Raw<true> r;
+        r.zero();
+        if (there(p)) r.load(a.g, 8 * (p * P + i0));
+        r.values(g);
+    };
+    auto parked = [&](int p, int h) { return reinterpret_cast<float4 *>(ring) + (2 * p + h) * blockDim.x + threadIdx.x; };
+#pragma unroll
+    for (int p = 0; p < V; p++) {
+        if (KEEP) {
+            load_weight(p, weight[KEEP ? p : 0]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) acc[KEEP ? p : 0][j] = 0.f;
+        } else {
+            *parked(p, 0) = *parked(p, 1) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    const float inverse = 1.f / (float)a.width;
+    int flip = 0, d = 0;
+    for (; t < a.n_tokens; t += step) {
+        uint32_t next[V];
+        scales(t + step, next);
+        if (D > 0) copies_wait<D - 1>();
+        const uint8_t *at = ring + d * V * slot;
+        auto values = [&](int p, float (&x)[8]) {
+            uint2 q = make_uint2(0u, 0u);
+            if (there(p))
+                q = D > 0 ? *reinterpret_cast<const uint2 *>(at + p * slot + 2 * kQ * P16 + me / 2)
+                          : reinterpret_cast<const uint2 *>(a.saved)[(int64_t)t * runs + p * P + i0];
+            from_e4m3x8(q, up_scale(scale[p]), x);
+        };
+        auto grads = [&](int p, int part, float (&v)[8]) {            // part 0: dn, 1: dres
+            Raw<BF16> r;
+            r.zero();
+            if (there(p)) {
+                if (D > 0) {
+#pragma unroll
+                    for (int q = 0; q < kQ; q++) r.q[q] = *reinterpret_cast<const uint4 *>(at + p * slot + (part * kQ + q) * P16 + me);
+                } else if (part == 0) {
+                    r.load(a.dn, t * a.lddn + 8 * (p * P + i0));
+                } else {
+                    r.load(a.dres, (int64_t)t * a.width + 8 * (p * P + i0));
+                }
+            }
+            r.values(v);
+        };
+        float x[KEEP ? V : 1][8], dn[KEEP ? V : 1][8], w[8];
+        if (KEEP) {
+#pragma unroll
+            for (int p = 0; p < V; p++) values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);
+        }
+        // a run's s, dn and weight: kept in registers, or fetched again
+        auto run = [&](int p, float (&rx)[8], float (&rd)[8], float (&rw)[8]) {
+            if (KEEP) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) rx[j] = x[KEEP ? p : 0][j], rd[j] = dn[KEEP ? p : 0][j], rw[j] = weight[KEEP ? p : 0][j];
+            } else {
+                values(p, rx), grads(p, 0, rd), load_weight(p, rw);
+            }
+        };
+        constexpr bool kEarly = KEEP && D == 0;              // dres with the rest, not after the sums
+        float early[8] = {};
+        if (kEarly && res) grads(0, 1, early);
         float ss, sx;
         auto sum = [&](float by) {
-            ss = sx = 0.f;
+            float2 s2 = both(0.f), x2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < V; p++) {
-                const uint32_t gw[4] = {gq[p].x, gq[p].y, gq[p].z, gq[p].w};
+                float rx[8], rd[8], rw[8];
+                run(p, rx, rd, rw);
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float gj = __uint_as_float(j & 1 ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
-                    const float v = x[p][j] * by;
-                    ss = fmaf(v, v, ss);
-                    sx = fmaf(gj * d[p][j], v, sx);
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 v = by == 1.f ? pair(rx, j) : __fmul2_rn(pair(rx, j), both(by));
+                    s2 = __ffma2_rn(v, v, s2);
+                    x2 = __ffma2_rn(__fmul2_rn(pair(rw, j), pair(rd, j)), v, x2);
                 }
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                sx += __shfl_xor_sync(0xffffffffu, sx, o);
-            }
+            float v = half_sums(s2.x + s2.y, x2.x + x2.y);
             if (!WARP) {
-                if (lane == 0) sums[flip][warp] = make_float2(ss, sx);
+                if ((lane & 15) == 0) sums[flip][lane >> 4][warp] = v;
                 __syncthreads();
-                const int nw = blockDim.x >> 5;
-                const float2 f = lane < nw ? sums[flip][lane] : make_float2(0.f, 0.f);
-                ss = f.x, sx = f.y;
+                const int nw = blockDim.x >> 5, l = lane & 15;
+                const float *row = sums[flip][lane >> 4];
+                v = (l < nw ? row[l] : 0.f) + (l + 16 < nw ? row[l + 16] : 0.f);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    sx += __shfl_xor_sync(0xffffffffu, sx, o);
-                }
+                for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                 flip ^= 1;
             }
+            ss = __shfl_sync(0xffffffffu, v, 0), sx = __shfl_sync(0xffffffffu, v, 16);
         };
         sum(1.f);
         float by = 1.f, eps = a.eps;
@@ -514,32 +633,56 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) k_norm_grad(const Norm
             by = 0x1p-72f, eps *= 0x1p-144f;
             sum(by);
         }
-        // k: the factor of the values times `by`
-        const float k = 1.f / sqrtf(ss / (float)a.width + eps);
-        const float q = k * (sx / (float)a.width), kx = k * by;
+        // k by: the factor of the values themselves, kq: dx = k a - n kq
+        const float m = fmaf(ss, inverse, eps), k0 = rsqrtf(m), k = m == 0.f ? k0 : k0 * fmaf(-0.5f, fmaf(m * k0, k0, -1.f), 1.f);
+        const float kx = k * by, kq = kx * (k * (sx * inverse));
 #pragma unroll
         for (int p = 0; p < V; p++) {
-            const int c = p * P + i0;
-            const uint32_t gw[4] = {gq[p].x, gq[p].y, gq[p].z, gq[p].w};
-            float r[8] = {};
-            if (a.dres != nullptr && c < runs) load8<BF16, true>(a.dres, t * a.width + 8 * c, r);
+            float rx[8], rd[8], rw[8], r[8] = {};
+            run(p, rx, rd, rw);
+            if (kEarly) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float gj = __uint_as_float(j & 1 ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
-                const float n = x[p][j] * by * k;
-                acc[p][j] = fmaf(d[p][j], n, acc[p][j]);
-                r[j] = fmaf(kx, fmaf(-n, q, gj * d[p][j]), r[j]);
+                for (int j = 0; j < 8; j++) r[j] = early[j];
+            } else if (res) {
+                grads(p, 1, r);
             }
-            store8<BF16>(a.dx, t * a.width + 8 * c, r, c < runs);
+            if (!KEEP) {
+                const float4 f = *parked(p, 0), g = *parked(p, 1);
+                acc[0][0] = f.x, acc[0][1] = f.y, acc[0][2] = f.z, acc[0][3] = f.w;
+                acc[0][4] = g.x, acc[0][5] = g.y, acc[0][6] = g.z, acc[0][7] = g.w;
+            }
+            float (&sum)[8] = acc[KEEP ? p : 0];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 n = __fmul2_rn(pair(rx, j), both(kx));
+                put(sum, j, __ffma2_rn(pair(rd, j), n, pair(sum, j)));
+                put(r, j, __ffma2_rn(n, both(-kq), __ffma2_rn(__fmul2_rn(pair(rw, j), pair(rd, j)), both(kx), pair(r, j))));
+            }
+            if (!KEEP) {
+                *parked(p, 0) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                *parked(p, 1) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            }
+            store8<BF16>(to_dx, 8 * p * P, r, there(p));
         }
+        to_dx += pitch * kElem;
+        if (D > 0) {
+            // (what was read of the slot has gone into the stores above)
+            fetch(base + d * V * slot);
+            d = d + 1 == D ? 0 : d + 1;
+        }
+#pragma unroll
+        for (int p = 0; p < V; p++) scale[p] = next[p];
     }
     float *to = gridDim.x == 1 ? a.dweight : a.part + (int64_t)blockIdx.x * a.width;
+    if (D > 0) copies_wait<0>();
     if (WARP) {
         // the eight warps' columns, added in their order
+        float *cols = reinterpret_cast<float *>(ring);
+        __syncthreads();
 #pragma unroll
         for (int p = 0; p < V; p++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) cols[warp * 256 * V + 8 * (p * 32 + lane) + j] = acc[p][j];
+            for (int j = 0; j < 8; j++) cols[warp * 256 * V + 8 * (p * 32 + lane) + j] = acc[KEEP ? p : 0][j];
         __syncthreads();
         for (int c = threadIdx.x; c < a.width; c += kThreads) {
             float s = 0.f;
@@ -549,25 +692,32 @@ __global__ void __launch_bounds__(WARP ? kThreads : 1024) k_norm_grad(const Norm
         }
     } else {
 #pragma unroll
-        for (int p = 0; p < V; p++) store8<false>(to, 8 * (p * P + i0), acc[p], p * P + i0 < runs);
+        for (int p = 0; p < V; p++) {
+            if (!KEEP) {
+                const float4 f = *parked(p, 0), g = *parked(p, 1);
+                acc[0][0] = f.x, acc[0][1] = f.y, acc[0][2] = f.z, acc[0][3] = f.w;
+                acc[0][4] = g.x, acc[0][5] = g.y, acc[0][6] = g.z, acc[0][7] = g.w;
+            }
+            store8<false>(to, 8 * (p * P + i0), acc[KEEP ? p : 0], there(p));
+        }
     }
 }
 
 // dweight[c] = sum over the parts: 32 columns a CTA, a share of the parts a warp
-__global__ void __launch_bounds__(kThreads) k_norm_grad_sum(float *dweight, const float *part, int parts, int width) {
-    __shared__ float sums[kThreads / 32][32];
+__global__ void __launch_bounds__(1024) k_norm_grad_sum(float *dweight, const float *part, int parts, int width) {
+    __shared__ float sums[32][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
 #pragma unroll 8
-    for (int p = warp; p < parts; p += kThreads / 32) s += part[(int64_t)p * width + c];      // width: whole blocks of 32
+    for (int p = warp; p < parts; p += warps) s += part[(int64_t)p * width + c];      // width: whole blocks of 32
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0) {
         s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; w++) s += sums[w][lane];
+#pragma unroll 8
+        for (int w = 0; w < warps; w++) s += sums[w][lane];
         dweight[c] = s;
     }
 }
@@ -610,19 +760,36 @@ size_t norm_grad_scratch_bytes(int n_tokens, int width) {
     return (size_t)norm_shape(n_tokens, width).parts * width * sizeof(float);
 }
 
-template <bool WARP, int V> static cudaError_t norm_grad_t(const Ctx &c, const NormGradArgs &a, const NormShape &s, int bf16) {
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(s.parts), dim3(s.threads), 0, c.stream, a); };
-    return bf16 ? go(k_norm_grad<WARP, V, true>) : go(k_norm_grad<WARP, V, false>);
+template <bool WARP, int V, int D, bool KEEP>
+static cudaError_t norm_grad_t(const Ctx &c, const NormGradArgs &a, const NormShape &s, int bf16) {
+    auto go = [&](auto kernel, std::atomic<uint64_t> &done) {
+        const int slots = D * V * run_bytes(bf16) * s.threads, sum = WARP || !KEEP ? s.threads * 8 * V * (int)sizeof(float) : 0;
+        const cudaError_t e = ensure_smem((const void *)kernel, kNormSmem, done);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(s.parts), dim3(s.threads), slots > sum ? slots : sum, c.stream, a);
+    };
+    static std::atomic<uint64_t> done_f32{0}, done_bf16{0};
+    return bf16 ? go(k_norm_grad<WARP, V, true, D, KEEP>, done_bf16) : go(k_norm_grad<WARP, V, false, D, KEEP>, done_f32);
 }
 
 cudaError_t launch_norm_grad(const Ctx &c, const NormGradArgs &a, int bf16) {
     const NormShape s = norm_shape(a.n_tokens, a.width);
-    cudaError_t e;
-    if (s.warp) e = s.v == 1 ? norm_grad_t<true, 1>(c, a, s, bf16) : norm_grad_t<true, 4>(c, a, s, bf16);
-    else e = s.v == 1 ? norm_grad_t<false, 1>(c, a, s, bf16) : s.v == 2 ? norm_grad_t<false, 2>(c, a, s, bf16)
-                                                                         : norm_grad_t<false, 4>(c, a, s, bf16);
+    const int row = s.threads * s.v * run_bytes(bf16);    // shared memory of a row
+    auto go = [&] {
+        if (s.warp)
+            return s.v == 1   ? norm_grad_t<true, 1, 4, true>(c, a, s, bf16)
+                   : s.v == 2 ? norm_grad_t<true, 2, 3, true>(c, a, s, bf16)
+                              : norm_grad_t<true, 4, 3, true>(c, a, s, bf16);
+        if (s.few) return norm_grad_t<false, 1, 0, true>(c, a, s, bf16);
+        if (s.threads <= 512)
+            return 4 * row <= kNormSmem   ? norm_grad_t<false, 2, 4, true>(c, a, s, bf16)
+                   : 3 * row <= kNormSmem ? norm_grad_t<false, 2, 3, true>(c, a, s, bf16)
+                                          : norm_grad_t<false, 2, 2, true>(c, a, s, bf16);
+        return s.v == 2 ? norm_grad_t<false, 2, 0, false>(c, a, s, bf16) : norm_grad_t<false, 4, 0, false>(c, a, s, bf16);
+    };
+    const cudaError_t e = go();
     if (e != cudaSuccess || s.parts == 1) return e;
-    return launch_pdl(k_norm_grad_sum, dim3(a.width / 32), dim3(kThreads), 0, c.stream, a.dweight, (const float *)a.part,
+    return launch_pdl(k_norm_grad_sum, dim3(a.width / 32), dim3(s.parts <= 64 ? 256 : 1024), 0, c.stream, a.dweight, (const float *)a.part,
                       s.parts, a.width);
 }
 
