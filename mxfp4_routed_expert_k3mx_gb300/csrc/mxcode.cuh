@@ -153,4 +153,42 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], uint8_t *codes, uint8
     return s;
 }
 
+__device__ __forceinline__ float at_least(float x, float least) {        // NaN stays NaN
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(least));
+    return y;
+}
+// Eight values as they lie in memory
+template <bool BF16> struct Raw {
+    uint4 q[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *base, int64_t i) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + i * (BF16 ? 2 : 4));
+        q[0] = p[0];
+        if (!BF16) q[BF16 ? 0 : 1] = p[1];
+    }
+    __device__ __forceinline__ void zero() { q[0] = q[BF16 ? 0 : 1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[BF16 ? 0 : 1].x, q[BF16 ? 0 : 1].y, q[BF16 ? 0 : 1].z, q[BF16 ? 0 : 1].w};
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] = __uint_as_float(!BF16 ? w[j] : j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+    }
+    // the values, but not below `least` (of which bf16 has whole numbers up to 256; NaN stays)
+    __device__ __forceinline__ void at_least_values(float least, float (&v)[8]) const {
+        if (BF16) {
+            Raw r;
+            const uint32_t l = bf16x2(least, least), w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+            uint32_t m[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m[j]) : "r"(w[j]), "r"(l));
+            r.q[0] = make_uint4(m[0], m[1], m[2], m[3]);
+            r.values(v);
+        } else {
+            values(v);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = at_least(v[j], least);
+        }
+    }
+};
+
 }  // namespace k3mx

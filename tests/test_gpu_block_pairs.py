@@ -44,7 +44,8 @@ def choices(T, K, n, drop, seed, skew=1.0):
 @pytest.mark.parametrize("T,K,n,drop", [
     (1, 1, 1, 0.0), (1, 16, 896, 0.0), (1, 16, 896, 1.0), (2, 3, 4, 0.3), (31, 1, 1024, 0.0), (33, 1, 5, 0.5), (64, 16, 896, 0.1),
     (1000, 7, 24, 0.2), (512, 16, 896, 0.0), (8192, 1, 3, 0.0), (8193, 1, 1, 0.0), (683, 12, 100, 0.9), (4096, 16, 896, 0.1),
-    (16385, 16, 1024, 0.0), (70001, 4, 37, 0.3), (300000, 1, 1024, 0.0), (1, 20000, 33, 0.1), (65536, 16, 896, 0.05)])
+    (16385, 16, 1024, 0.0), (70001, 4, 37, 0.3), (300000, 1, 1024, 0.0), (1, 20000, 33, 0.1), (65536, 16, 896, 0.05), (256, 1, 9, 0.1), (257, 1, 9, 0.1), (2048, 1, 50, 0.0), (2049, 1, 50, 0.1),
+    (4096, 1, 50, 0.0), (4097, 1, 50, 0.1), (16384, 1, 7, 0.0), (16385, 1, 7, 0.1), (65537, 1, 33, 0.0), (131073, 1, 33, 0.1)])
 def test_sort(cuda_dev, T, K, n, drop):
     idx = choices(T, K, n, drop, seed=T + K)
     offsets, perm, place = sorted_pairs(torch.from_numpy(idx).to(DEV), n)
@@ -65,18 +66,18 @@ def test_sort(cuda_dev, T, K, n, drop):
 
 
 def test_sort_without_perm_and_with_a_larger_workspace(cuda_dev):
-    idx = torch.from_numpy(choices(3000, 5, 60, 0.1, 1)).to(DEV)
+    idx = torch.from_numpy(choices(30000, 5, 60, 0.1, 1)).to(DEV)
     want = sorted_pairs(idx, 60)
-    offsets, place = i32(61), i32(3000, 5)
+    offsets, place = i32(61), i32(30000, 5)
     k3mx.k3mx_sort(offsets, None, place, idx, torch.empty(1 << 16, dtype=torch.int64, device=DEV))
     assert torch.equal(offsets, want[0]) and torch.equal(place, want[2])
     few = torch.zeros(3, 2, dtype=torch.int32, device=DEV)
     k3mx.k3mx_sort(i32(61), None, i32(3, 2), few, None)
     with pytest.raises(k3mx.K3mxError, match="EWORKSPACE"):
-        k3mx.k3mx_sort(i32(61), None, i32(3000, 5), idx, None)
+        k3mx.k3mx_sort(i32(61), None, i32(30000, 5), idx, None)
 
 
-@pytest.mark.parametrize("T", [5, 5000])
+@pytest.mark.parametrize("T", [5, 5000, 30000, 100000])
 def test_sort_reports_a_bad_expert_and_drops_its_pair(cuda_dev, T):
     idx = choices(T, 2, 9, 0.0, 3)
     good = idx.copy()
@@ -250,6 +251,20 @@ def test_rows_that_begin_off_sixteen_bytes(cuda_dev, off):
     assert torch.equal(dr, ds) and torch.allclose(dw, dv, rtol=1e-5, atol=1e-5)
     k3mx.k3mx_dispatch(rows, x, place)
     assert torch.equal(rows[0], x[0]) and torch.equal(rows[2], x[0]) and torch.equal(rows[1], x[1])
+
+
+@pytest.mark.parametrize("off,xoff", [(1, 0), (0, 3), (7, 9), (16, 4)])
+def test_codes_that_begin_off_sixteen_bytes(cuda_dev, off, xoff):
+    place, R = placed(9, 40, 0.3, off)                     # (more pairs a token than are listed at a time)
+    gen = torch.Generator(device=DEV).manual_seed(off)
+    u8 = lambda n: torch.randint(0, 256, (n,), generator=gen, device=DEV, dtype=torch.uint8)
+    x, xs = u8(9 * 4224 + xoff)[xoff:].view(9, 4224), u8(9 * 132 + xoff)[xoff:].view(9, 132)
+    rows, scales = u8(R * 4224 + off)[off:].view(R, 4224), u8(R * 132 + off)[off:].view(R, 132)
+    want, ws = rows.cpu().clone(), scales.cpu().clone()
+    k3mx.k3mx_dispatch(rows, x, torch.from_numpy(place).to(DEV), scales=scales, x_scales=xs)
+    t, k = np.nonzero(place >= 0)
+    want[place[t, k]], ws[place[t, k]] = x.cpu()[t], xs.cpu()[t]
+    assert torch.equal(rows.cpu(), want) and torch.equal(scales.cpu(), ws)
 
 
 def test_offsets_past_32_bits(cuda_dev):
