@@ -7,11 +7,13 @@ quantises the expert weights to MXFP4 once, then per step
 
   sum, codes = rmsnorm(x + residual)        k3mx_rmsnorm_mx (bf16 copy for the router)
   idx, w     = router(normed)               k3mx_router
-  offsets    = grouping of the pairs        k3mx_group
-  g | u      = W13[e] x per pair            k3mx_mx_grouped
-  h          = SiTU-GLU(g, u) in MXFP8      k3mx_mx_quantize
+  place      = pairs by expert              k3mx_sort
+  xe         = the tokens' codes by pair    k3mx_dispatch
+  g | u      = W13[e] xe                    k3mx_mx_grouped
+  h          = SiTU-GLU(g, u) in MXFP8      k3mx_mx_quantize (of any activation; k3mx_situ_mx is this one in one step)
   rows       = W2[e] h per pair             k3mx_mx_grouped
-  y          = sum_k w_k rows + Ws x        k3mx_mx_linear (a dense branch beside the experts)
+  y          = Ws x                         k3mx_mx_linear (a dense branch beside the experts)
+  out        = y + sum_k w_k rows           k3mx_combine
 
 The router's shapes (hidden 7168, 896 experts, top 16) are the library's; the
 experts' and the dense branch's widths are free.
@@ -68,10 +70,10 @@ class Block:
         k3mx.k3mx_rmsnorm_mx(r["codes"], r["scales"], r["sum"], x, residual, self.norm, EPS, normed=r["normed"])
         r["logits"], r["idx"], r["w"] = torch.empty(T, EXPERTS, device="cuda"), i32(T, TOPK), torch.empty(T, TOPK, device="cuda")
         k3mx.k3mx_router(r["logits"], r["idx"], r["w"], r["normed"], self.router, self.bias)
-        r["offsets"], r["perm"] = i32(EXPERTS + 1), i32(P)
-        k3mx.k3mx_group(i32(EXPERTS), r["offsets"], r["perm"], r["idx"], u8(k3mx.k3mx_group_workspace_size(T)))
-        r["token"] = r["perm"].long() // TOPK
-        xc, xs = r["codes"][r["token"]], r["scales"][r["token"]]
+        r["offsets"], r["perm"], r["place"] = i32(EXPERTS + 1), i32(P), i32(T, TOPK)
+        k3mx.k3mx_sort(r["offsets"], r["perm"], r["place"], r["idx"], u8(k3mx.k3mx_sort_workspace_size(T, TOPK, EXPERTS)))
+        xc, xs = u8(P, HIDDEN), u8(P, HIDDEN // 32)
+        k3mx.k3mx_dispatch(xc, r["codes"], r["place"], scales=xs, x_scales=r["scales"])
         r["gu"] = torch.empty(P, 2 * self.inter, device="cuda")
         k3mx.k3mx_mx_grouped(r["gu"], xc, xs, *self.w13, r["offsets"])
         g, u = r["gu"].chunk(2, dim=1)
@@ -81,7 +83,7 @@ class Block:
         k3mx.k3mx_mx_grouped(r["rows"], r["hcodes"], r["hscales"], *self.w2, r["offsets"])
         r["y"] = torch.empty(T, HIDDEN, device="cuda")
         k3mx.k3mx_mx_linear(r["y"], r["codes"], r["scales"], *self.dense)
-        r["out"] = r["y"].index_add(0, r["token"], r["rows"] * r["w"].reshape(-1)[r["perm"].long()][:, None])
+        r["out"] = k3mx.k3mx_combine(torch.empty_like(r["y"]), r["rows"], r["place"], w=r["w"], base=r["y"])
         return r
 
 
