@@ -8,6 +8,7 @@ namespace k3mx {
 namespace {
 
 constexpr int kThreads = 256;
+#define ST_THREADS 1024
 constexpr int kSituCtas = 3, kSituWaves = 4;    // CTAs of k_situ an SM holds, and the rounds of them in its grid
 
 // 8 e4m3 codes -> their values times `up`
@@ -48,6 +49,8 @@ __device__ __forceinline__ float reciprocal(float x) {
     return y;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const float (&v)[8], int j) { return make_float2(v[j], v[j + 1]); }
+__device__ __forceinline__ void put(float (&v)[8], int j, float2 f) { v[j] = f.x, v[j + 1] = f.y; }
 __device__ __forceinline__ float2 exp2_approx(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
 __device__ __forceinline__ float2 reciprocal(float2 x) { return make_float2(reciprocal(x.x), reciprocal(x.y)); }
 
@@ -122,17 +125,25 @@ __device__ void exp_two(float xh, float xl, Two &E, Two &less, Two &more) {
     less = plus_low(two(1.f, -E.h), -E.l);
     if (n == 0.f) less = {-m.h, -m.l};
 }
-// ... rounded to the odd one of its two fp32 neighbours, so that rounding it
-// on to a code rounds h itself
-__device__ __noinline__ float situ_odd(float g, float u) {
-    g = at_least(g, kLeastG), u = at_least(u, kLeastU);
-    Two E, F, ng, dg, nu, du;
-    exp_two(-0.5f * g, 0.f, E, ng, dg);
+// a(g) and b(u) (for g >= kLeastG, u >= kLeastU and not above 100 and 700,
+// where they have their limits to 2^-48)
+__device__ __forceinline__ Two situ_a(float g) {
+    Two E, n, d;
+    exp_two(-0.5f * g, 0.f, E, n, d);
+    const Two E2 = times(E, E), c = plus_low(two(1.f, E2.h), E2.l);
+    return times(over(n, d), over(Two{4.f, 0.f}, c));
+}
+__device__ __forceinline__ Two situ_b(float u) {
+    Two F, n, d;
     constexpr float k = -0.08f;
     const float xh = __fmul_rn(u, k);
-    exp_two(xh, fmaf(u, k, -xh) + u * (float)(-0.08 - (double)k), F, nu, du);
-    const Two E2 = times(E, E), c = plus_low(two(1.f, E2.h), E2.l);
-    const Two h = times(times(over(ng, dg), over(nu, du)), over(Two{100.f, 0.f}, c));
+    exp_two(xh, fmaf(u, k, -xh) + u * (float)(-0.08 - (double)k), F, n, d);
+    return times(over(n, d), Two{25.f, 0.f});
+}
+// h of g and u that are not NaN, rounded to the odd one of its two fp32
+// neighbours, so that rounding it on to a code rounds h itself
+__device__ __noinline__ float situ_odd(float g, float u) {
+    const Two h = times(situ_a(fminf(fmaxf(g, kLeastG), 100.f)), situ_b(fminf(fmaxf(u, kLeastU), 700.f)));
     const uint32_t bits = __float_as_uint(h.h);
     if (h.l == 0.f || (bits & 1u)) return h.h;
     return __uint_as_float((h.l < 0.f) == (h.h < 0.f) ? bits + 1 : bits - 1);
@@ -148,21 +159,17 @@ __device__ __noinline__ float situ_odd(float g, float u) {
 // and where g < -16 the value may be further off: there a code may be the other
 // of two neighbours.)
 constexpr uint32_t kNear = 88;        // units of 2^-24: 64 + 1.5 * 16
-constexpr double kBias = kNear / 16777216.0;
+constexpr double bias_of(uint32_t units) { return units / 16777216.0; }
 __device__ __forceinline__ uint32_t above_middle(float v) { return (__float_as_uint(v) ^ 0x80000u) & 0xFFFFFu; }
-__device__ __forceinline__ void encode_situ(const float (&g)[8], const float (&u)[8], uint8_t *codes, uint8_t *scales, int64_t i, bool live) {
-    float h[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float2 p = situ2(make_float2(g[j], g[j + 1]), make_float2(u[j], u[j + 1]), kBias);
-        h[j] = p.x, h[j + 1] = p.y;
-    }
+// NEAR: the units of h's bias; g, u: the values by place, for those formed again
+template <uint32_t NEAR, typename G, typename U>
+__device__ __forceinline__ void encode_situ(float (&h)[8], G g, U u, uint8_t *codes, uint8_t *scales, int64_t i, bool live) {
     uint32_t mb = block_max(h);
-    const bool scale_near = ((mb ^ 0x600000u) & 0x7FFFFFu) <= 2 * kNear && mb < 0x7F800000u;
+    const bool scale_near = ((mb ^ 0x600000u) & 0x7FFFFFu) <= 2 * NEAR && mb < 0x7F800000u;
     if (__any_sync(0xffffffffu, scale_near)) {
         if (scale_near) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) h[j] = situ_odd(g[j], u[j]);
+            for (int j = 0; j < 8; j++) h[j] = situ_odd(g(j), u(j));
         }
         mb = block_max(h);
     }
@@ -174,10 +181,10 @@ __device__ __forceinline__ void encode_situ(const float (&g)[8], const float (&u
         least = min(least, above_middle(h[j]));
         h[j] *= down;
     }
-    if (least <= 2 * kNear && s != 255u) {
+    if (least <= 2 * NEAR && s != 255u) {
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            if (above_middle(h[j]) <= 2 * kNear) h[j] = situ_odd(g[j], u[j]) * down;
+            if (above_middle(h[j]) <= 2 * NEAR) h[j] = situ_odd(g(j), u(j)) * down;
     }
     const uint32_t keep = s == 255u ? 0u : 0xFFFFFFFFu;
     if (live) {
@@ -227,8 +234,98 @@ __global__ void __launch_bounds__(kThreads, kSituCtas) k_situ(const SituArgs a, 
         float g[8], u[8];
         rg.at_least_values(kLeastG, g);
         ru.at_least_values(kLeastU, u);
-        encode_situ(g, u, a.codes, a.scales, k, live);
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) put(h, j, situ2(pair(g, j), pair(u, j), bias_of(kNear)));
+        encode_situ<kNear>(h, [&](int j) { return g[j]; }, [&](int j) { return u[j]; }, a.codes, a.scales, k, live);
         if (SAVE) {
+            rg.values(g);
+            ru.values(u);
+            encode8<K3MX_MXFP8>(g, a.saved, a.saved_scales, sg, live);
+            encode8<K3MX_MXFP8>(u, a.saved, a.saved_scales, sg + runs, live);
+        }
+    }
+}
+
+// Many runs of bf16.  bf16 has 128 values a binade, so a(g) for 2^-14 <= |g| < 2^7
+// and b(u) for 2^-13 <= |u| < 2^9 are tables of fp32 values in shared memory,
+// each rounded once, looked up by the value's bits; h is their product, within 4
+// units of 2^-24 of itself, and hardly any value has to be formed again.  Places
+// are clamped to the tables; a value that this changed (zeros, Inf and NaN among
+// them) is worked out by itself.
+constexpr int kLowG = (127 - 14) * 128, kCountG = 21 * 128, kLowU = (127 - 13) * 128, kCountU = 22 * 128;
+constexpr uint32_t kNearTable = 6;
+constexpr int kSituTableThreads = ST_THREADS;
+constexpr int64_t kSituTableRuns = 1 << 20;
+
+__device__ __noinline__ float situ_apart(float g, float u) {
+    if (g != g || u != u) return __uint_as_float(0x7FC00000u);
+    const float zero = __uint_as_float((__float_as_uint(g) ^ __float_as_uint(u)) & 0x80000000u);
+    return g == 0.f || u == 0.f ? zero : situ_odd(g, u);
+}
+
+template <bool SAVE>
+__global__ void __launch_bounds__(kSituTableThreads, 1024 / kSituTableThreads) k_situ_table(const SituArgs a, int64_t n8, int runs) {
+    __shared__ float ta[2 * kCountG], tb[kCountU];        // ta: g > 0, then g < 0
+    pdl_wait();
+    pdl_launch_dependents();
+    int64_t i = (int64_t)blockIdx.x * kSituTableThreads + threadIdx.x;
+    const int64_t stride = (int64_t)gridDim.x * kSituTableThreads;
+    Walk at(i, stride, runs);
+    Raw<true> ng, nu;
+    auto fetch = [&] {
+        ng.zero(), nu.zero();
+        if (i < n8) {
+            ng.load(a.gu, at.r * a.ldgu + 8 * at.c);
+            nu.load(a.gu, at.r * a.ldgu + 8 * (at.c + runs));
+        }
+    };
+    fetch();
+    for (int e = threadIdx.x; e < 2 * kCountG + kCountU; e += kSituTableThreads) {
+        if (e < 2 * kCountG) {
+            const float v = __uint_as_float((uint32_t)(kLowG + (e < kCountG ? e : e - kCountG)) << 16);
+            ta[e] = situ_a(e < kCountG ? v : -v).h;
+        } else {
+            const float v = __uint_as_float((uint32_t)(kLowU + e - 2 * kCountG) << 16);
+            tb[e - 2 * kCountG] = situ_b(v).h * (float)(1.0 + bias_of(kNearTable));
+        }
+    }
+    __syncthreads();
+    for (; i - threadIdx.x < n8;) {
+        const Raw<true> rg = ng, ru = nu;
+        const int64_t k = i;
+        const bool live = k < n8;
+        const int64_t sg = (int64_t)at.r * 2 * runs + at.c;
+        i += stride;
+        at.next();
+        fetch();
+        const uint32_t wg[4] = {rg.q[0].x, rg.q[0].y, rg.q[0].z, rg.q[0].w}, wu[4] = {ru.q[0].x, ru.q[0].y, ru.q[0].z, ru.q[0].w};
+        auto value = [](const uint32_t (&w)[4], int j) {
+            return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+        };
+        float h[8];
+        uint32_t out = 0;                              // differs from 0 where a place was clamped
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t mg = wg[j] & 0x7FFF7FFFu, mu = wu[j] & 0x7FFF7FFFu;
+            const uint32_t cg = __vminu2(__vmaxu2(mg, kLowG * 0x10001u), (kLowG + kCountG - 1) * 0x10001u);
+            const uint32_t cu = __vminu2(__vmaxu2(mu, kLowU * 0x10001u), (kLowU + kCountU - 1) * 0x10001u);
+            out |= (cg ^ mg) | (cu ^ mu);
+            const uint32_t pg = cg + ((wg[j] >> 15) & 0x10001u) * (uint32_t)kCountG;
+            h[2 * j] = ta[(pg & 0xFFFFu) - kLowG] * __uint_as_float(__float_as_uint(tb[(cu & 0xFFFFu) - kLowU]) ^ (wu[j] << 16 & 0x80000000u));
+            h[2 * j + 1] = ta[(pg >> 16) - kLowG] * __uint_as_float(__float_as_uint(tb[(cu >> 16) - kLowU]) ^ (wu[j] & 0x80000000u));
+        }
+        if (out != 0) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t mg = (j & 1 ? wg[j >> 1] >> 16 : wg[j >> 1]) & 0x7FFFu, mu = (j & 1 ? wu[j >> 1] >> 16 : wu[j >> 1]) & 0x7FFFu;
+                if (mg - kLowG >= kCountG || mu - kLowU >= kCountU) h[j] = situ_apart(value(wg, j), value(wu, j));
+            }
+        }
+        __syncwarp();
+        encode_situ<kNearTable>(h, [&](int j) { return value(wg, j); }, [&](int j) { return value(wu, j); }, a.codes, a.scales, k, live);
+        if (SAVE) {
+            float g[8], u[8];
             rg.values(g);
             ru.values(u);
             encode8<K3MX_MXFP8>(g, a.saved, a.saved_scales, sg, live);
@@ -439,8 +536,6 @@ __device__ __forceinline__ float half_sums(float a, float b) {
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float2 pair(const float (&v)[8], int j) { return make_float2(v[j], v[j + 1]); }
-__device__ __forceinline__ void put(float (&v)[8], int j, float2 f) { v[j] = f.x, v[j + 1] = f.y; }
 
 template <bool WARP, int V, bool BF16, int D, bool KEEP>
 __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_grad(const NormGradArgs a) {
@@ -692,6 +787,13 @@ cudaError_t launch_situ(const Ctx &c, const SituArgs &a, int bf16) {
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kThreads), 0, c.stream, a, n8, runs);
     };
+    if (bf16 && n8 >= kSituTableRuns) {
+        const int64_t per = kSituTableThreads, all = (n8 + per - 1) / per, fit = (int64_t)c.num_sms * (1024 / per);
+        auto table = [&](auto kernel) {
+            return launch_pdl(kernel, dim3((unsigned)(all < fit ? all : fit)), dim3(kSituTableThreads), 0, c.stream, a, n8, runs);
+        };
+        return a.saved != nullptr ? table(k_situ_table<true>) : table(k_situ_table<false>);
+    }
     if (a.saved != nullptr) return bf16 ? go(k_situ<true, true>) : go(k_situ<false, true>);
     return bf16 ? go(k_situ<true, false>) : go(k_situ<false, false>);
 }

@@ -96,6 +96,66 @@ def test_situ_of_extreme_values(cuda_dev):
     assert np.all(doubles(dgu)[0].reshape(2, 7, 32)[0, 3:5] == 0) and k3mx.k3mx_device_status() == (0, 0)
 
 
+@pytest.mark.parametrize("kind", sorted(TYPES))
+def test_situ_where_one_factor_is_a_limit(cuda_dev, kind):
+    """h = 4 b(u) and 25 a(g), of many values: some are near the middle of two codes."""
+    r = np.random.default_rng(7)
+    for other in (1.0, -1.0):
+        x = np.concatenate([np.full((512, 256), np.inf), r.normal(size=(512, 256)) * 8], 1)
+        for gate in (True, False):
+            if not gate:
+                x = np.concatenate([x[:, 256:], other * x[:, :256]], 1)
+            gu = rows_of(x, kind, 0)
+            codes, scales, _, _ = situ(gu, False)
+            g, u = doubles(gu)[:, :256], doubles(gu)[:, 256:]
+            want, s = mx_ref.quantize(block_ref.situ(np.minimum(g, 1e3), np.clip(u, -1e4, 1e4)), mx_ref.MXFP8)
+            got = codes.cpu().numpy()
+            assert np.array_equal(scales.cpu().numpy(), s)
+            assert np.array_equal(np.where(want & 127 >= 8, want, 0), np.where(got & 127 >= 8, got, 0))
+
+
+@pytest.mark.parametrize("save", [False, True])
+def test_situ_of_many_rows(cuda_dev, save):
+    """Every bf16 value of g with some of u and the other way round, in a call of
+    many rows and in calls of few."""
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    r = np.random.default_rng(8)
+    R, F = 16640, 512                                             # (1 M runs and more)
+    x = torch.from_numpy(r.normal(size=(R, 2 * F)) * np.exp(r.normal(size=(1, 2 * F)))).bfloat16()
+    finite = every[torch.isfinite(every.float())]
+    n = finite.numel() // 32 * 32
+    x[:n // 32, :32] = finite[:n].view(-1, 32)                     # g
+    x[:n // 32, F + 32:F + 64] = finite[:n].view(-1, 32)           # u
+    x[4000:4128, :F] = every.view(128, 512)
+    x[5000:5128, F:] = every.view(128, 512)
+    x[6000:6500] = 0
+    x[6500:7000, ::3] = 0
+    gu = x.to(DEV)
+    out = situ(gu, save)
+    v = doubles(gu)
+    g, u = v[:, :F], v[:, F:]
+    with np.errstate(all="ignore"):
+        h = np.where(np.isnan(g) | np.isnan(u), np.nan, block_ref.situ(np.clip(g, -700, 1e3), np.clip(u, -1e4, 1e4)))
+        # blocks with g < -16, where codes may be others', and those whose largest is next to nothing
+        dim = (np.abs(np.nan_to_num(h)).reshape(R, F // 32, 32).max(-1) < 2.0 ** -90) | (g.reshape(R, F // 32, 32).min(-1) < -16)
+    want, s = mx_ref.quantize(np.where(np.isnan(h), np.nan, h), mx_ref.MXFP8)
+    got = out[0].cpu().numpy()
+    assert np.array_equal(out[1].cpu().numpy()[~dim], s[~dim])
+    bright = ~dim.repeat(32, 1).reshape(R, F)
+    assert np.array_equal(got[bright & (want & 127 >= 8)], want[bright & (want & 127 >= 8)])
+    for at in (slice(0, 4200), slice(5000, 5200), slice(6000, 7100), slice(16000, R)):
+        few = situ(gu[at].contiguous(), save)
+        assert np.array_equal(few[1].cpu().numpy()[~dim[at]], s[at][~dim[at]])
+        a, b = (np.where(bright[at], t, 0) for t in (few[0].cpu().numpy(), got[at]))
+        # (codes below 2^-6 may be the other of two neighbours)
+        assert np.mean(a != b) < 2e-4 and np.abs((a & 127).astype(int) - (b & 127)).max() <= 1
+        assert not save or (torch.equal(few[2], out[2][at]) and torch.equal(few[3], out[3][at]))
+    if save:
+        code, s = mx_ref.quantize(v, mx_ref.MXFP8)
+        assert np.array_equal(out[2].cpu().numpy(), code) and np.array_equal(out[3].cpu().numpy(), s)
+    assert k3mx.k3mx_device_status() == (0, 0)
+
+
 def test_situ_of_tiny_and_zero_blocks(cuda_dev):
     x = np.zeros((3, 128))
     x[1] = 1e-38
