@@ -56,8 +56,8 @@ k3mx_status k3mx_sort(int32_t *offsets, int32_t *perm, int32_t *place, const int
  *          for K3MX_E4M3 (width a multiple of 32), else both NULL
  *   place  [n_tokens][topk] as k3mx_sort writes it: -1 is skipped, another
  *          value outside 0..n_rows-1 too, and k3mx_device_status reports
- *          K3MX_EINVAL with the pair; a row that two pairs name holds one of
- *          the two
+ *          K3MX_EINVAL with the pair; a row that two tokens' pairs name holds
+ *          parts of either
  *   rows   [n_rows][width] and scales: rows that no pair names are left as
  *          they are
  *   n_tokens * topk <= K3MX_BLOCK_MAX_PAIRS, 1 <= n_rows <= K3MX_MX_MAX_ROWS,
@@ -90,7 +90,8 @@ k3mx_status k3mx_combine(void *y, int y_dtype, const void *rows, int rows_dtype,
  *   dw = sum_c dy[t][c] rows[place][c] (fp32; 0 for a skipped pair).
  *   dy    [n_tokens] rows, lddy elements apart (width <= lddy <= 2^32)
  *   drows [n_rows][width] of rows' type; rows that no pair names are left as
- *         they are; may be rows itself where no two pairs name one row
+ *         they are (one that two pairs name holds parts of either's); may be
+ *         rows itself where no two pairs name one row
  *   dw    [n_tokens][topk]
  *   otherwise as k3mx_combine
  */
@@ -114,7 +115,7 @@ k3mx_status k3mx_combine_backward(void *drows, float *dw, const void *dy, int64_
  *   of 16 bytes.
  * What is saved is exactly k3mx_mx_quantize's.  The codes and scales of h are
  * those that k3mx_mx_quantize's definition gives for h itself, formed within
- * 2^-29; but a code below 2^-6 (a value under 2^-15 of its block's largest), and
+ * 2^-29 where |h| > 2^-96; but a code below 2^-6 (a value under 2^-15 of its block's largest), and
  * any where g < -16, is that of a value within 2^-15 of h, and where g < -87
  * h may be taken for 0.  Infinite g and u have their limits; a NaN makes its
  * block NaN.

@@ -125,9 +125,10 @@ __device__ void exp_two(float xh, float xl, Two &E, Two &less, Two &more) {
     less = plus_low(two(1.f, -E.h), -E.l);
     if (n == 0.f) less = {-m.h, -m.l};
 }
-// a(g) and b(u) (for g >= kLeastG, u >= kLeastU and not above 100 and 700,
-// where they have their limits to 2^-48)
+// a(g) and b(u) (for g <= 100 and kLeastU <= u <= 700, where they have their
+// limits to 2^-48); a is taken for 0 where E^2 leaves fp32
 __device__ __forceinline__ Two situ_a(float g) {
+    if (g < -87.f) return {-0.f, 0.f};
     Two E, n, d;
     exp_two(-0.5f * g, 0.f, E, n, d);
     const Two E2 = times(E, E), c = plus_low(two(1.f, E2.h), E2.l);
@@ -143,7 +144,7 @@ __device__ __forceinline__ Two situ_b(float u) {
 // h of g and u that are not NaN, rounded to the odd one of its two fp32
 // neighbours, so that rounding it on to a code rounds h itself
 __device__ __noinline__ float situ_odd(float g, float u) {
-    const Two h = times(situ_a(fminf(fmaxf(g, kLeastG), 100.f)), situ_b(fminf(fmaxf(u, kLeastU), 700.f)));
+    const Two h = times(situ_a(fminf(g, 100.f)), situ_b(fminf(fmaxf(u, kLeastU), 700.f)));
     const uint32_t bits = __float_as_uint(h.h);
     if (h.l == 0.f || (bits & 1u)) return h.h;
     return __uint_as_float((h.l < 0.f) == (h.h < 0.f) ? bits + 1 : bits - 1);
@@ -767,8 +768,13 @@ __global__ void __launch_bounds__(1024) k_norm_grad_sum(float *dweight, const fl
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
-#pragma unroll 8
-    for (int p = warp; p < parts; p += warps) s += part[(int64_t)p * width + c];      // width: whole blocks of 32
+    for (int p0 = warp; p0 < parts; p0 += 8 * warps) {
+        float v[8];                   // loads at once, the last ones of the last part again
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = part[(int64_t)min(p0 + j * warps, parts - 1) * width + c];      // width: whole blocks of 32
+#pragma unroll
+        for (int j = 0; j < 8; j++) s += p0 + j * warps < parts ? v[j] : 0.f;
+    }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0) {

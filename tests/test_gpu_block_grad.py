@@ -130,18 +130,24 @@ def test_situ_of_many_rows(cuda_dev, save):
     x[5000:5128, F:] = every.view(128, 512)
     x[6000:6500] = 0
     x[6500:7000, ::3] = 0
+    x[7000:9000, 64:72] *= 300                                     # outliers beside ordinary values
     gu = x.to(DEV)
     out = situ(gu, save)
     v = doubles(gu)
     g, u = v[:, :F], v[:, F:]
     with np.errstate(all="ignore"):
         h = np.where(np.isnan(g) | np.isnan(u), np.nan, block_ref.situ(np.clip(g, -700, 1e3), np.clip(u, -1e4, 1e4)))
-        # blocks with g < -16, where codes may be others', and those whose largest is next to nothing
-        dim = (np.abs(np.nan_to_num(h)).reshape(R, F // 32, 32).max(-1) < 2.0 ** -90) | (g.reshape(R, F // 32, 32).min(-1) < -16)
+        # blocks whose largest is next to nothing, or has g < -16 (there codes may be others')
+        m, low = np.abs(np.nan_to_num(h)).reshape(R, F // 32, 32), (g < -16).reshape(R, F // 32, 32)
+        top = np.where(low, 0, m).max(-1)
+        dim = (top < 2.0 ** -90) | (top < m.max(-1))
     want, s = mx_ref.quantize(np.where(np.isnan(h), np.nan, h), mx_ref.MXFP8)
     got = out[0].cpu().numpy()
     assert np.array_equal(out[1].cpu().numpy()[~dim], s[~dim])
+    assert np.array_equal(out[1].cpu().numpy() == 255, s == 255)
     bright = ~dim.repeat(32, 1).reshape(R, F)
+    assert np.abs((got & 127).astype(int) - (want & 127))[bright].max() <= 1
+    bright &= ~low.reshape(R, F)
     assert np.array_equal(got[bright & (want & 127 >= 8)], want[bright & (want & 127 >= 8)])
     for at in (slice(0, 4200), slice(5000, 5200), slice(6000, 7100), slice(16000, R)):
         few = situ(gu[at].contiguous(), save)
@@ -284,6 +290,27 @@ def test_norm_backward(cuda_dev, T, W, kind):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     check_norm(*norm_backward(x, dn, w, 0.5, None, kind), kind, T, W)
     assert k3mx.k3mx_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("T,W", [(1 << 21, 32), (200_000, 1056)])
+def test_norm_backward_of_very_many_rows(cuda_dev, T, W):
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    saved = torch.randint(0, 0x78, (T, W), generator=gen, device=DEV, dtype=torch.uint8)
+    ss = torch.randint(118, 122, (T, W // 32), generator=gen, device=DEV, dtype=torch.uint8)
+    dn, g = torch.randn(T, W, generator=gen, device=DEV) + 0.5, torch.ones(W, device=DEV).bfloat16()
+    dx, dw = torch.empty(T, W, device=DEV), torch.empty(W, device=DEV)
+    ws = u8(k3mx.k3mx_rmsnorm_mx_backward_workspace_size(T, W))
+    k3mx.k3mx_rmsnorm_mx_backward(dx, dw, dn, saved, ss, g, 1e-5, ws)
+    x = saved.view(torch.float8_e4m3fn).double().view(T, W // 32, 32) * torch.exp2(ss.double() - 127)[..., None]
+    x = x.view(T, W)
+    n = x / torch.sqrt(x.square().mean(1, keepdim=True) + 1e-5)
+    want, mag = (dn.double() * n).sum(0), (dn.double() * n).abs().sum(0)
+    # 1024 rows in turn at most, then 2048 parts by 32 warps, 64 in turn, and those
+    assert torch.all((dw - want).abs() <= (1024 + 64 + 32 + 40) * 2.0 ** -24 * mag)
+    at = torch.tensor([0, 1, T // 2, T - 1], device=DEV)
+    a, q = dn[at].double(), (dn[at].double() * n[at]).mean(1, keepdim=True)
+    k = 1 / torch.sqrt(x[at].square().mean(1, keepdim=True) + 1e-5)
+    assert torch.all((dx[at] - k * (a - n[at] * q)).abs() <= 100 * 2.0 ** -24 * k * (a.abs() + n[at].abs() * (a * n[at]).abs().mean(1, keepdim=True)))
 
 
 def test_norm_backward_with_the_forward_pass(cuda_dev):

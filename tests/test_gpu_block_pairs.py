@@ -65,6 +65,20 @@ def test_sort(cuda_dev, T, K, n, drop):
     assert np.array_equal(place.cpu().numpy().reshape(-1), want)
 
 
+@pytest.mark.parametrize("T,K", [(1 << 24, 1), (1 << 20, 16)])
+def test_sort_of_the_most_pairs(cuda_dev, T, K):
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    idx = torch.randint(-1, 1024, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    offsets, perm, place = sorted_pairs(idx, 1024)
+    key, order = torch.sort(torch.where(idx < 0, torch.full_like(idx, 1024), idx).reshape(-1), stable=True)
+    n = int(offsets[-1])
+    assert torch.equal(offsets.long(), torch.searchsorted(key, torch.arange(1025, device=DEV, dtype=torch.int32)))
+    assert torch.equal(perm[:n].long(), order[:n]) and torch.all(perm[n:] == -7)
+    want = torch.full((T * K,), -1, dtype=torch.int32, device=DEV)
+    want[order[:n]] = torch.arange(n, dtype=torch.int32, device=DEV)
+    assert torch.equal(place.reshape(-1), want) and k3mx.k3mx_device_status() == (0, 0)
+
+
 def test_sort_without_perm_and_with_a_larger_workspace(cuda_dev):
     idx = torch.from_numpy(choices(30000, 5, 60, 0.1, 1)).to(DEV)
     want = sorted_pairs(idx, 60)
