@@ -115,10 +115,9 @@ k3mx_status k3mx_combine_backward(void *drows, float *dw, const void *dy, int64_
  *   of 16 bytes.
  * What is saved is exactly k3mx_mx_quantize's.  The codes and scales of h are
  * those that k3mx_mx_quantize's definition gives for h itself, formed within
- * 2^-29 where |h| > 2^-96; but a code below 2^-6 (a value under 2^-15 of its block's largest), and
- * any where g < -16, is that of a value within 2^-15 of h, and where g < -87
- * h may be taken for 0.  Infinite g and u have their limits; a NaN makes its
- * block NaN.
+ * 2^-29 where |h| > 2^-96; but where g < -16 they are those of a value within
+ * 2^-15 of h, and where g < -87 h may be taken for 0.  Infinite g and u have
+ * their limits; a NaN makes its block NaN.
  */
 k3mx_status k3mx_situ_mx(uint8_t *codes, uint8_t *scales, uint8_t *saved, uint8_t *saved_scales,
                          const void *gu, int64_t ldgu, int dtype, int rows, int inter, k3mx_stream_t stream);

@@ -1,5 +1,17 @@
 // block.cu - pairs (a token and one of its choices) in the order of their
 // experts, tokens' rows taken to their pairs' places, and back with weights.
+//
+// All of it moves data: what counts is that each row is read and written once,
+// in whole vectors, with enough of them on their way, and for few tokens that
+// a call is one latency after another as seldom as can be.  Measured (repeated
+// calls, inputs larger than L2; a copy reaches 6.78 TB/s):
+//   dispatch 4096 tokens x 16, 3584 MXFP8      37.1 us, 6.3 TB/s; 1 token 1.6 us
+//   combine 65536 rows of 3584 fp32            129 us, 7.0 TB/s; bf16 76 us, 6.6
+//   combine 1 token, 16 rows of 7168 bf16      1.7 us
+//   its gradient, 65536 rows of 3584 bf16      155 us, 6.3 TB/s; 1 token 2.2 us
+// Rows that do not begin at multiples of 16 bytes (an odd width) take an element
+// at a time but for dispatch: 32768 rows of 3001 bf16 combined in 136 us (36 by
+// their bytes), fp32 50 for 16384; their gradient in 100 us (62 by its bytes).
 #include <type_traits>
 
 #include "blockops.cuh"

@@ -56,15 +56,11 @@ def test_situ(cuda_dev, R, F, kind, pad):
     assert np.array_equal(saved.cpu().numpy(), code) and np.array_equal(ss.cpu().numpy(), s)
     g, u = x[:, :F], x[:, F:]
     h = block_ref.situ(g, u)
-    # h's own codes, but for the smallest (values near a middle are formed within 2^-29: one in 30 million may still turn)
+    # h's own codes (values near a middle are formed within 2^-29: one in 30 million may still turn); below g = -16 a neighbour's
     want, s = mx_ref.quantize(h, mx_ref.MXFP8)
     got = codes.cpu().numpy()
     assert np.array_equal(scales.cpu().numpy(), s)
-    assert np.array_equal(np.where(want & 127 >= 8, want, 0), np.where(got & 127 >= 8, got, 0))
-    # those: half a step of 2^-9, and the 2^-15 that h is off by there (64 + 1.5 * 87 units of 2^-24 and as much of bias: 2^-15.4)
-    e = np.exp2(s.astype(np.float64) - 127).repeat(32, 1).reshape(R, F)
-    off = np.abs(mx_ref.values(got, s, mx_ref.MXFP8) - h)
-    assert np.all((off <= 2.0 ** -10 * e + 2.0 ** -15 * np.abs(h)) | (want & 127 >= 8))
+    assert np.array_equal(got[g >= -16], want[g >= -16]) and np.abs((got & 127).astype(int) - (want & 127)).max() <= 1
     alone = situ(gu, False)
     assert torch.equal(alone[0], codes) and torch.equal(alone[1], scales)
     assert k3mx.k3mx_device_status() == (0, 0)
@@ -111,7 +107,7 @@ def test_situ_where_one_factor_is_a_limit(cuda_dev, kind):
             want, s = mx_ref.quantize(block_ref.situ(np.minimum(g, 1e3), np.clip(u, -1e4, 1e4)), mx_ref.MXFP8)
             got = codes.cpu().numpy()
             assert np.array_equal(scales.cpu().numpy(), s)
-            assert np.array_equal(np.where(want & 127 >= 8, want, 0), np.where(got & 127 >= 8, got, 0))
+            assert np.array_equal(got[g >= -16], want[g >= -16])
 
 
 @pytest.mark.parametrize("save", [False, True])
@@ -148,13 +144,11 @@ def test_situ_of_many_rows(cuda_dev, save):
     bright = ~dim.repeat(32, 1).reshape(R, F)
     assert np.abs((got & 127).astype(int) - (want & 127))[bright].max() <= 1
     bright &= ~low.reshape(R, F)
-    assert np.array_equal(got[bright & (want & 127 >= 8)], want[bright & (want & 127 >= 8)])
+    assert np.array_equal(got[bright], want[bright])
     for at in (slice(0, 4200), slice(5000, 5200), slice(6000, 7100), slice(16000, R)):
         few = situ(gu[at].contiguous(), save)
         assert np.array_equal(few[1].cpu().numpy()[~dim[at]], s[at][~dim[at]])
-        a, b = (np.where(bright[at], t, 0) for t in (few[0].cpu().numpy(), got[at]))
-        # (codes below 2^-6 may be the other of two neighbours)
-        assert np.mean(a != b) < 2e-4 and np.abs((a & 127).astype(int) - (b & 127)).max() <= 1
+        assert np.array_equal(few[0].cpu().numpy()[bright[at]], got[at][bright[at]])
         assert not save or (torch.equal(few[2], out[2][at]) and torch.equal(few[3], out[3][at]))
     if save:
         code, s = mx_ref.quantize(v, mx_ref.MXFP8)
