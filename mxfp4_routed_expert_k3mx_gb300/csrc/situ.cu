@@ -3,7 +3,7 @@
 // own and the RMSNorm's.
 //
 // Measured (repeated calls, inputs larger than L2; a copy reaches 6.78 TB/s):
-//   SiTU 65536 x 2048 bf16, saved       247 us, 3.9 TB/s; not saved 182 us
+//   SiTU 65536 x 2048 bf16, saved       242 us, 3.9 TB/s; not saved 177 us
 //   SiTU 32768 x 2048 fp32, saved       139 us, 5.4 TB/s
 //   its gradient, 65536 x 2048 bf16     173 us, 6.3 TB/s; 32768 fp32 150 us, 6.3
 //   norm's gradient, 4096 x 7168 bf16   40 us, 5.2 TB/s; fp32 88 us, 4.4
@@ -318,12 +318,15 @@ __global__ void __launch_bounds__(kSituTableThreads, 1024 / kSituTableThreads) k
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const uint32_t mg = wg[j] & 0x7FFF7FFFu, mu = wu[j] & 0x7FFF7FFFu;
-            const uint32_t cg = __vminu2(__vmaxu2(mg, kLowG * 0x10001u), (kLowG + kCountG - 1) * 0x10001u);
-            const uint32_t cu = __vminu2(__vmaxu2(mu, kLowU * 0x10001u), (kLowU + kCountU - 1) * 0x10001u);
-            out |= (cg ^ mg) | (cu ^ mu);
-            const uint32_t pg = cg + ((wg[j] >> 15) & 0x10001u) * (uint32_t)kCountG;
-            h[2 * j] = ta[(pg & 0xFFFFu) - kLowG] * __uint_as_float(__float_as_uint(tb[(cu & 0xFFFFu) - kLowU]) ^ (wu[j] << 16 & 0x80000000u));
-            h[2 * j + 1] = ta[(pg >> 16) - kLowG] * __uint_as_float(__float_as_uint(tb[(cu >> 16) - kLowU]) ^ (wu[j] & 0x80000000u));
+            // the place, clamped, and that of the bits as they are
+            const uint32_t cg = __viaddmin_s16x2_relu(mg, (65536u - kLowG) * 0x10001u, (kCountG - 1) * 0x10001u);
+            const uint32_t cu = __viaddmin_s16x2_relu(mu, (65536u - kLowU) * 0x10001u, (kCountU - 1) * 0x10001u);
+            out |= (cg ^ (mg - kLowG * 0x10001u)) | (cu ^ (mu - kLowU * 0x10001u));
+            // byte offsets, two to a word; the negative g's are behind the others
+            const uint32_t og = cg * 4u + ((wg[j] >> 15) & 0x10001u) * (4u * kCountG), ou = cu * 4u;
+            auto at = [](const float *t, uint32_t o) { return *reinterpret_cast<const float *>(reinterpret_cast<const char *>(t) + o); };
+            h[2 * j] = at(ta, og & 0xFFFFu) * __uint_as_float(__float_as_uint(at(tb, ou & 0xFFFFu)) ^ (wu[j] << 16 & 0x80000000u));
+            h[2 * j + 1] = at(ta, og >> 16) * __uint_as_float(__float_as_uint(at(tb, ou >> 16)) ^ (wu[j] & 0x80000000u));
         }
         if (out != 0) {
 #pragma unroll
