@@ -9,9 +9,11 @@
 //   combine 65536 rows of 3584 fp32            129 us, 7.0 TB/s; bf16 76 us, 6.6
 //   combine 1 token, 16 rows of 7168 bf16      1.7 us
 //   its gradient, 65536 rows of 3584 bf16      155 us, 6.3 TB/s; 1 token 2.2 us
-// Rows that do not begin at multiples of 16 bytes (an odd width) take an element
-// at a time but for dispatch: 32768 rows of 3001 bf16 combined in 136 us (36 by
-// their bytes), fp32 50 for 16384; their gradient in 100 us (62 by its bytes).
+// Rows that do not begin at multiples of 16 bytes (an odd width) are put together
+// from whole vectors by dispatch and by combine of bf16 (32768 rows of 3001 in 83
+// us, 136 an element at a time, 36 by their bytes); fp32 (16384 rows of 3001 in 50
+// us, 36 by their bytes) and the gradient (32768 of bf16 in 100 us, 62 by its
+// bytes) take an element at a time.
 #include <type_traits>
 
 #include "blockops.cuh"
@@ -549,6 +551,77 @@ __global__ void __launch_bounds__(kThreads) k_combine_few(const CombineArgs a, i
     }
 }
 
+// Rows of bf16 that begin anywhere, in an array that begins at 16 bytes: a
+// thread's eight columns are put together from two of the array's vectors by one
+// shift for all of a row (its second vector is the next thread's first, and
+// comes from L1).  What a CTA has summed goes through shared memory, so that y,
+// which may begin anywhere too, is written by neighbouring threads.
+template <bool YB>
+__global__ void __launch_bounds__(128) k_combine_shift(const CombineArgs a, int chunks) {
+    constexpr int U = 4;
+    __shared__ Listed list[kListed];
+    __shared__ int listed;
+    __shared__ float4 out[256];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t = blockIdx.x / chunks, end = (int64_t)a.n_rows * a.width;       // elements of rows
+    const int chunk = (int)(blockIdx.x - t * chunks), c0 = chunk * 8 * blockDim.x, c = c0 + 8 * threadIdx.x;
+    float acc[8] = {};
+    for (int k0 = 0; k0 < a.topk; k0 += kListed) {
+        if (k0 > 0) __syncthreads();
+        if (threadIdx.x < 32)
+            list_rows(list, &listed, a.place, t, true, a.topk, a.n_rows, k0, chunk == 0, a.status,
+                      [&](int r, int64_t p) { return Listed{(int64_t)r * a.width, a.w != nullptr ? a.w[p] : 1.f}; });
+        __syncthreads();
+        const int n = c < a.width ? listed : 0;
+        for (int j0 = 0; j0 < n; j0 += U) {
+            uint4 lo[U], hi[U];
+#pragma unroll
+            for (int j = 0; j < U; j++)
+                if (j0 + j < n) {
+                    const int64_t v = (list[j0 + j].at + c) >> 3;                   // the first vector with a column of ours
+                    auto vector = [&](int64_t i) {
+                        if (8 * (i + 1) <= end) return static_cast<const uint4 *>(a.rows)[i];
+                        // the array ends inside it
+                        uint32_t w[4] = {};
+                        for (int e = 0; e < 8 && 8 * i + e < end; e++)
+                            w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(a.rows)[8 * i + e] << 16 * (e & 1);
+                        return make_uint4(w[0], w[1], w[2], w[3]);
+                    };
+                    lo[j] = vector(v);
+                    hi[j] = vector(v + 1);
+                }
+#pragma unroll
+            for (int j = 0; j < U; j++)
+                if (j0 + j < n) {
+                    const int from = (int)list[j0 + j].at & 7;                     // elements
+                    const float w = list[j0 + j].w;
+                    uint32_t q[8] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
+                    const uint32_t sel = from & 1 ? 0x5432u : 0x3210u;
+#pragma unroll
+                    for (int i = 0; i < 6; i++) q[i] = from & 4 ? q[i + 2] : q[i];
+#pragma unroll
+                    for (int i = 0; i < 5; i++) q[i] = from & 2 ? q[i + 1] : q[i];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t b = __byte_perm(q[i], q[i + 1], sel);
+                        acc[2 * i] = fmaf(w, __uint_as_float(b << 16), acc[2 * i]);
+                        acc[2 * i + 1] = fmaf(w, __uint_as_float(b & 0xFFFF0000u), acc[2 * i + 1]);
+                    }
+                }
+        }
+    }
+    out[2 * threadIdx.x] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    out[2 * threadIdx.x + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * (int)blockDim.x && c0 + i < a.width; i += blockDim.x) {
+        float s[1] = {reinterpret_cast<const float *>(out)[i]}, b[1] = {0.f};
+        if (a.base != nullptr) load_run<YB, 1>(a.base, t * a.width + c0 + i, b);
+        s[0] += b[0];
+        store_run<YB, 1>(a.y, t * a.width + c0 + i, s);
+    }
+}
+
 // Rows that begin anywhere: four columns a thread, a CTA's threads apart, so
 // that a row's address is worked out once for the four.
 template <bool RB, bool YB>
@@ -726,6 +799,12 @@ cudaError_t launch_dispatch(const Ctx &c, const DispatchArgs &a) {
 
 template <bool RB, bool YB> static cudaError_t combine_t(const Ctx &c, const CombineArgs &a) {
     if (a.width % 8 != 0 || !multiple16(a.rows) || !multiple16(a.y) || !multiple16(a.base)) {
+        if constexpr (RB)
+            if (multiple16(a.rows)) {
+                const int runs = (a.width + 7) / 8, chunks = (runs + 63) / 64, threads = ((runs + chunks - 1) / chunks + 31) / 32 * 32;
+                return launch_pdl(k_combine_shift<YB>, dim3((unsigned)((int64_t)a.n_tokens * chunks)), dim3(threads), 0, c.stream, a,
+                                  chunks);
+            }
         int threads = (a.width + 3) / 4;
         threads = threads < kThreads ? (threads + 31) / 32 * 32 : kThreads;
         const int chunks = (a.width + 4 * threads - 1) / (4 * threads);

@@ -80,8 +80,9 @@ template <int C> __device__ __forceinline__ float2 tanh_series(float2 x, double 
 // the bias each is within (64 + 1.5 |g|) units of 2^-24 of h for g >= -87,
 // where 1 + E^2 has a normal reciprocal: an exponential is off by 4 units and
 // by 0.75 |g| of its argument's rounding, its square by twice that, of which
-// 1 + E^2 has at most all (8 + 1.5 |g|); 1 - E by at most 17 at |g| = 1/2, and
-// 1 + E by 4; the same for F; the two reciprocals and the products by 9.
+// 1 + E^2 has at most all (9 + 1.5 |g| rounded); (1 - E) / (1 + E) by four times
+// an exponential's error at |g| = 1/2, and two roundings, 20, and 19 for F; the
+// two reciprocals by 4, products and constants by 5.
 __device__ __forceinline__ float2 situ2(float2 g, float2 u, double bias) {
     const double scale = 100.0 * (1.0 + bias);
     const float2 E = exp2_approx(__fmul2_rn(g, both((float)(-0.5 * kLog2e))));
