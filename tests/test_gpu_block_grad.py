@@ -270,7 +270,7 @@ def check_norm(dx, dweight, want, kind, T, W):
     assert np.all(np.abs(doubles(dweight) - wg) <= (rows + W / 1024 + 40) * 2.0 ** -24 * mg + 1e-40)
 
 
-@pytest.mark.parametrize("T,W", [(1, 32), (1, 7168), (3, 64), (8, 256), (9, 288), (64, 1024), (65, 1056), (700, 160), (613, 2048),
+@pytest.mark.parametrize("T,W", [(1, 32), (1, 7168), (2, 7168), (2, 16416), (16, 128), (17, 1024), (3, 64), (8, 256), (9, 288), (64, 1024), (65, 1056), (700, 160), (613, 2048),
                                  (200, 7168), (33, 8224), (7, 16384), (5, 16416), (3, 32768), (5000, 96), (2500, 1536)])
 @pytest.mark.parametrize("kind", sorted(TYPES))
 def test_norm_backward(cuda_dev, T, W, kind):
