@@ -10,10 +10,10 @@
 //   combine 1 token, 16 rows of 7168 bf16      1.7 us
 //   its gradient, 65536 rows of 3584 bf16      155 us, 6.3 TB/s; 1 token 2.2 us
 // Rows that do not begin at multiples of 16 bytes (an odd width) are put together
-// from whole vectors by dispatch and by combine of bf16 (32768 rows of 3001 in 83
-// us, 136 an element at a time, 36 by their bytes); fp32 (16384 rows of 3001 in 50
-// us, 36 by their bytes) and the gradient (32768 of bf16 in 100 us, 62 by its
-// bytes) take an element at a time.
+// from whole vectors by dispatch and, of bf16, by combine (32768 rows of 3001 in 83
+// us, 136 an element at a time, 36 by their bytes) and its gradient (77 us, 100,
+// 62); fp32 rows (16384 of 3001 combined in 50 us, 36 by their bytes) and other
+// types take an element at a time.
 #include <type_traits>
 
 #include "blockops.cuh"
@@ -551,6 +551,26 @@ __global__ void __launch_bounds__(kThreads) k_combine_few(const CombineArgs a, i
     }
 }
 
+// Vector i of an array of 16-bit elements that begins at 16 bytes and has `end`
+// of them, zeros behind it
+__device__ __forceinline__ uint4 vector_of(const void *base, int64_t i, int64_t end) {
+    if (8 * (i + 1) <= end) return static_cast<const uint4 *>(base)[i];
+    uint32_t w[4] = {};
+    for (int e = 0; e < 8 && 8 * i + e < end; e++) w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(base)[8 * i + e] << 16 * (e & 1);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// eight elements from the one `from` (0..7) of two neighbouring vectors on, two to a word
+__device__ __forceinline__ void shifted(uint4 lo, uint4 hi, int from, uint32_t (&b)[4]) {
+    uint32_t q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint32_t sel = from & 1 ? 0x5432u : 0x3210u;
+#pragma unroll
+    for (int i = 0; i < 6; i++) q[i] = from & 4 ? q[i + 2] : q[i];
+#pragma unroll
+    for (int i = 0; i < 5; i++) q[i] = from & 2 ? q[i + 1] : q[i];
+#pragma unroll
+    for (int i = 0; i < 4; i++) b[i] = __byte_perm(q[i], q[i + 1], sel);
+}
+
 // Rows of bf16 that begin anywhere, in an array that begins at 16 bytes: a
 // thread's eight columns are put together from two of the array's vectors by one
 // shift for all of a row (its second vector is the next thread's first, and
@@ -580,33 +600,20 @@ __global__ void __launch_bounds__(128) k_combine_shift(const CombineArgs a, int 
             for (int j = 0; j < U; j++)
                 if (j0 + j < n) {
                     const int64_t v = (list[j0 + j].at + c) >> 3;                   // the first vector with a column of ours
-                    auto vector = [&](int64_t i) {
-                        if (8 * (i + 1) <= end) return static_cast<const uint4 *>(a.rows)[i];
-                        // the array ends inside it
-                        uint32_t w[4] = {};
-                        for (int e = 0; e < 8 && 8 * i + e < end; e++)
-                            w[e >> 1] |= (uint32_t)static_cast<const uint16_t *>(a.rows)[8 * i + e] << 16 * (e & 1);
-                        return make_uint4(w[0], w[1], w[2], w[3]);
-                    };
-                    lo[j] = vector(v);
-                    hi[j] = vector(v + 1);
+                    lo[j] = vector_of(a.rows, v, end);
+                    hi[j] = vector_of(a.rows, v + 1, end);
                 }
 #pragma unroll
             for (int j = 0; j < U; j++)
                 if (j0 + j < n) {
                     const int from = (int)list[j0 + j].at & 7;                     // elements
                     const float w = list[j0 + j].w;
-                    uint32_t q[8] = {lo[j].x, lo[j].y, lo[j].z, lo[j].w, hi[j].x, hi[j].y, hi[j].z, hi[j].w};
-                    const uint32_t sel = from & 1 ? 0x5432u : 0x3210u;
-#pragma unroll
-                    for (int i = 0; i < 6; i++) q[i] = from & 4 ? q[i + 2] : q[i];
-#pragma unroll
-                    for (int i = 0; i < 5; i++) q[i] = from & 2 ? q[i + 1] : q[i];
+                    uint32_t b[4];
+                    shifted(lo[j], hi[j], from, b);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const uint32_t b = __byte_perm(q[i], q[i + 1], sel);
-                        acc[2 * i] = fmaf(w, __uint_as_float(b << 16), acc[2 * i]);
-                        acc[2 * i + 1] = fmaf(w, __uint_as_float(b & 0xFFFF0000u), acc[2 * i + 1]);
+                        acc[2 * i] = fmaf(w, __uint_as_float(b[i] << 16), acc[2 * i]);
+                        acc[2 * i + 1] = fmaf(w, __uint_as_float(b[i] & 0xFFFF0000u), acc[2 * i + 1]);
                     }
                 }
         }
@@ -725,6 +732,70 @@ __global__ void __launch_bounds__(kThreads, M) k_combine_grad(const CombineGradA
     }
 }
 
+// The same for bf16 rows that begin anywhere in arrays that begin at 16 bytes: a
+// row and its gradient have whole vectors at the same places, and elements at
+// both ends; the token's gradient is put together by one shift for all.  (32768
+// rows of 3001: 77 us, 100 an element at a time, 92 with registers for four CTAs
+// an SM and not six.)
+__global__ void __launch_bounds__(kThreads, 6) k_combine_grad_shift(const CombineGradArgs a, int n_pairs) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int kAtOnce = kThreads / 32;
+    const int lane = threadIdx.x & 31;
+    int p = blockIdx.x * kAtOnce + (threadIdx.x >> 5);
+    const int64_t dend = (int64_t)(a.n_tokens - 1) * a.lddy + a.width;
+    int at = -1;
+    float w = 0.f;
+    auto look = [&](int p) {
+        at = p < n_pairs ? a.place[p] : -1;
+        w = p < n_pairs ? a.w[p] : 0.f;
+    };
+    look(p);
+    for (; p < n_pairs; p += gridDim.x * kAtOnce) {
+        const int r = row_of(at, a.n_rows, lane == 0, p, a.status);
+        const float wp = w;
+        look(p + gridDim.x * kAtOnce);
+        float acc[2] = {};
+        if (r >= 0) {
+            const int64_t from = (int64_t)r * a.width, dfrom = (int64_t)(p / a.topk) * a.lddy;
+            const int head = min(a.width, (int)(-from & 7)), vectors = (a.width - head) / 8, tail = head + 8 * vectors;
+            const uint4 *rows = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.rows) + from + head);
+            uint4 *drows = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.drows) + from + head);
+            const int64_t d0 = (dfrom + head) >> 3;
+            const int shift = (int)(dfrom + head) & 7;
+#pragma unroll 1
+            for (int v = lane; v < vectors; v += 32) {
+                const uint4 x = rows[v], lo = vector_of(a.dy, d0 + v, dend), hi = vector_of(a.dy, d0 + v + 1, dend);
+                uint32_t b[4], o[4];
+                shifted(lo, hi, shift, b);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float d0 = __uint_as_float(b[i] << 16), d1 = __uint_as_float(b[i] & 0xFFFF0000u);
+                    acc[0] = fmaf(__uint_as_float(xw[i] << 16), d0, acc[0]);
+                    acc[1] = fmaf(__uint_as_float(xw[i] & 0xFFFF0000u), d1, acc[1]);
+                    o[i] = bf16x2(wp * d0, wp * d1);
+                }
+                drows[v] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            // the elements before and behind, at most seven each
+            const int c = lane < 8 ? lane : tail + lane - 8;
+            if (lane < 8 ? c < head : lane < 16 && c < a.width) {
+                float x[1], d[1];
+                load_run<true, 1>(a.rows, from + c, x);
+                load_run<true, 1>(a.dy, dfrom + c, d);
+                acc[0] = fmaf(x[0], d[0], acc[0]);
+                d[0] *= wp;
+                store_run<true, 1>(a.drows, from + c, d);
+            }
+        }
+        float dot = acc[0] + acc[1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) a.dw[p] = dot;
+    }
+}
+
 bool multiple16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <typename S> cudaError_t dispatch_t(const Ctx &c, const DispatchArgs &a, int units, int64_t ld, int scale_units) {
@@ -839,6 +910,8 @@ template <bool RB, bool DB> static cudaError_t combine_grad_t(const Ctx &c, cons
     };
     const bool wide = a.width % 8 == 0 && a.lddy % 8 == 0 && multiple16(a.rows) && multiple16(a.drows) && multiple16(a.dy);
     const bool few = n <= 4 * c.num_sms;                  // (16 pairs of 7168 bf16: 2.2 us, 4 by a warp each)
+    if constexpr (RB && DB)
+        if (!wide && !few && multiple16(a.rows) && multiple16(a.drows) && multiple16(a.dy)) return go(k_combine_grad_shift, 8, 6);
     if (!wide) return few ? go(k_combine_grad<RB, DB, 1, 8, 4, 4>, 1, 0) : go(k_combine_grad<RB, DB, 1, 1, 8, 4>, 8, 4);
     if (few) return go(k_combine_grad<RB, DB, 8, 8, 2, 4>, 1, 0);
     // bf16: many warps with a run each in flight (65536 x 3584 155 us, 182 with

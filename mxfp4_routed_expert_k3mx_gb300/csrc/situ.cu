@@ -19,7 +19,7 @@ namespace k3mx {
 namespace {
 
 constexpr int kThreads = 256;
-#define ST_THREADS 1024
+
 constexpr int kSituCtas = 3, kSituWaves = 4;    // CTAs of k_situ an SM holds, and the rounds of them in its grid
 
 // 8 e4m3 codes -> their values times `up`
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kSituCtas) k_situ(const SituArgs a, 
 // them) is worked out by itself.
 constexpr int kLowG = (127 - 14) * 128, kCountG = 21 * 128, kLowU = (127 - 13) * 128, kCountU = 22 * 128;
 constexpr uint32_t kNearTable = 6;
-constexpr int kSituTableThreads = ST_THREADS;
+constexpr int kSituTableThreads = 1024;       // (two CTAs of 512, with a table each, take 5 % more)
 constexpr int64_t kSituTableRuns = 1 << 20;
 
 __device__ __noinline__ float situ_apart(float g, float u) {
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_g
             }
             r.values(v);
         };
-        float x[KEEP ? V : 1][8], dn[KEEP ? V : 1][8], w[8];
+        float x[KEEP ? V : 1][8], dn[KEEP ? V : 1][8];
         if (KEEP) {
 #pragma unroll
             for (int p = 0; p < V; p++) values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);

@@ -125,7 +125,7 @@ def placed(T, K, drop, seed, extra=3):
 
 
 SHAPES = [(1, 1, 1), (1, 16, 3584), (1, 2, 7168), (3, 5, 1), (7, 3, 33), (5, 4, 64), (64, 2, 8), (300, 6, 1000), (257, 1, 1001),
-          (33, 17, 520), (2, 64, 4100), (1024, 8, 256), (70, 40, 4096), (5000, 33, 64), (9, 40, 33)]
+          (33, 17, 520), (2, 64, 4100), (1024, 8, 256), (70, 40, 4096), (5000, 33, 64), (9, 40, 33), (300, 5, 1001), (700, 2, 9), (1000, 1, 5)]
 
 
 @pytest.mark.parametrize("T,K,W", SHAPES)
