@@ -44,9 +44,11 @@ __device__ __forceinline__ float up_scale(uint32_t s) {
 // a(g) = 4 tanh(g/4) sigma(g) and b(u) = 25 tanh(u/25), h = a b.  With E =
 // exp(-g/2) and F = exp(-2u/25):
 //   h = 4 (1 - E) / (1 + E) / (1 + E^2) * 25 (1 - F) / (1 + F),
-// two exponentials and two reciprocals, for either sign and without an
-// overflow once g >= -130 and u >= -250 (E^2 may be infinite: its reciprocal
-// is the limit, 0).  Where 1 - E cancels (|g| < 1/2, |u| < 25/8) tanh is its
+// two exponentials and two reciprocals, for either sign.  g and u are taken for
+// no less than -110 and -250 first: E is below 2^80 and F below 2^29 then, so
+// that the two numerators' product, 2^116 at most, and that of the denominators
+// stay finite (E^2 is infinite below g = -88.7: its reciprocal is the limit, 0).
+// Where 1 - E cancels (|g| < 1/2, |u| < 25/8) tanh is its
 // series at 0 instead, times the 1 + E that the reciprocal divides by.
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -66,7 +68,7 @@ __device__ __forceinline__ float2 exp2_approx(float2 x) { return make_float2(exp
 __device__ __forceinline__ float2 reciprocal(float2 x) { return make_float2(reciprocal(x.x), reciprocal(x.y)); }
 
 constexpr double kLog2e = 1.4426950408889634;
-constexpr float kLeastG = -130.f, kLeastU = -250.f;
+constexpr float kLeastG = -110.f, kLeastU = -250.f;
 // x P(x^2) = tanh(x/C) up to x = C/8: y (1 - y^2/3 + 2y^4/15 - ..), what
 // follows is below 3.5 units of 2^-24
 template <int C> __device__ __forceinline__ float2 tanh_series(float2 x, double scale) {

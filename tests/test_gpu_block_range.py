@@ -1,0 +1,68 @@
+"""The activation and the norm's gradient at the ends of their inputs' range,
+against the double-precision definitions."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref
+import mx_ref
+import mxfp4_routed_expert_k3mx_gb300 as k3mx
+from test_gpu_block_grad import TYPES, doubles, rows_of, situ
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+INF, NAN = float("inf"), float("nan")
+
+
+def situ_of(g, u):
+    """h in doubles, with its limits."""
+    with np.errstate(all="ignore"):
+        return np.where(np.isnan(g) | np.isnan(u), np.nan, block_ref.situ(np.clip(g, -700, 1e3), np.clip(u, -1e4, 1e4)))
+
+
+# ---------------------------------------------------------- the activation --
+
+GATES = [INF, 3e38, 1000, 130, 30, 1, 2.0 ** -20, 0.0, -0.0, -2.0 ** -20, -1, -16, -40, -86, -87, -88, -89, -100, -110, -111, -128,
+         -128.5, -129, -130, -131, -200, -250, -300, -1000, -3e38, -INF, NAN]
+UPS = [INF, 3e38, 1000, 512, 250, 25, 1, 0.0, -0.0, -1, -25, -230, -239, -240, -249, -250, -251, -256, -286, -288, -290, -300, -512, -700,
+       -1000, -3e38, -INF, NAN]
+
+
+@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("many", [False, True])
+def test_situ_of_every_extreme_with_every_other(cuda_dev, kind, many):
+    """Whole blocks of one pair of values, and single pairs beside ordinary ones."""
+    r = np.random.default_rng(11)
+    g, u = (v.reshape(-1) for v in np.meshgrid(GATES, UPS, indexing="ij"))
+    n = g.size                                               # 896 pairs: 28 blocks of each of 32 rows
+    whole = [np.repeat(v.reshape(32, 28), 32, axis=1) for v in (g, u)]
+    beside = [r.normal(size=(32, 896)) * 3 for _ in range(2)]
+    at = r.integers(0, 32, size=n).reshape(32, 28) + 32 * np.arange(28)
+    for v, w in zip(beside, (g, u)):
+        np.put_along_axis(v, at, w.reshape(32, 28), axis=1)
+    x = np.concatenate([np.concatenate(whole, 1), np.concatenate(beside, 1)])
+    if many:                                                 # (1 M runs and more of bf16 take another form)
+        x = np.concatenate([x, r.normal(size=(9400 - 64, 2 * 896)).astype(np.float32)])
+    gu = rows_of(x, kind, 8)
+    codes, scales, _, _ = situ(gu, False)
+    v = doubles(gu)[:64]
+    g, u = v[:, :896], v[:, 896:]
+    h = situ_of(g, u)
+    want, s = mx_ref.quantize(h, mx_ref.MXFP8)
+    got, gs = codes.cpu().numpy()[:64], scales.cpu().numpy()[:64]
+    assert np.array_equal(gs == 255, np.isnan(h).reshape(64, 28, 32).any(-1))
+    # values: a code's half step, 2^-15 below g = -16, and 100 e^-87 where h may be taken for 0; half the smallest
+    # code's step of the block
+    top = np.nanmax(np.abs(np.where(np.isnan(h), 0.0, h)).reshape(64, 28, 32), -1).repeat(32, 1)
+    live = ~(gs == 255).repeat(32, 1)
+    val = mx_ref.values(got, gs, mx_ref.MXFP8)
+    tol = (2.0 ** -4 + 2.0 ** -14) * np.abs(h) + 2.0 ** -17 * top + 2.0 ** -118
+    assert np.all(np.abs(val - h)[live] <= tol[live])
+    # h's own codes under its own scale, unless the block's largest is one of those
+    mag, low = np.abs(h).reshape(64, 28, 32), (g < -16).reshape(64, 28, 32)
+    top = np.where(low, 0.0, mag).max(-1)
+    bright = (top >= 2.0 ** -90) & (top >= mag.max(-1))
+    assert np.array_equal(gs[bright], s[bright])
+    exact = bright.repeat(32, 1) & ~(g < -16)
+    assert np.array_equal(got[exact], want[exact])
+    assert k3mx.k3mx_device_status() == (0, 0)
