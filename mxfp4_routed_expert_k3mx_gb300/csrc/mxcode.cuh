@@ -173,7 +173,7 @@ template <bool BF16> struct Raw {
         for (int j = 0; j < 8; j++)
             v[j] = __uint_as_float(!BF16 ? w[j] : j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
     }
-    // the values, but not below `least` (of which bf16 has whole numbers up to 256; NaN stays)
+    // the values, but not below `least` (a value that bf16 has; NaN stays)
     __device__ __forceinline__ void at_least_values(float least, float (&v)[8]) const {
         if (BF16) {
             Raw r;

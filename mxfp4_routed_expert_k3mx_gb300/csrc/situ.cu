@@ -45,11 +45,11 @@ __device__ __forceinline__ float up_scale(uint32_t s) {
 // exp(-g/2) and F = exp(-2u/25):
 //   h = 4 (1 - E) / (1 + E) / (1 + E^2) * 25 (1 - F) / (1 + F),
 // two exponentials and two reciprocals, for either sign.  g and u are taken for
-// no less than -110 and -250 first: E is below 2^80 and F below 2^29 then, so
-// that the two numerators' product, 2^116 at most, and that of the denominators
-// stay finite (E^2 is infinite below g = -88.7: its reciprocal is the limit, 0).
-// Where 1 - E cancels (|g| < 1/2, |u| < 25/8) tanh is its
-// series at 0 instead, times the 1 + E that the reciprocal divides by.
+// no less than -110 and -288 first: E is below 2^80 and F below 2^34 then, so
+// that the two numerators' product, 2^121 at most, and that of the denominators
+// stay finite (E^2 is infinite below g = -88.7: its reciprocal is the limit, 0;
+// b(-288) is its limit to 2^-32).  Where 1 - E cancels (|g| < 1/2, |u| < 25/8)
+// tanh is its series at 0 instead, times the 1 + E that the reciprocal divides by.
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -68,7 +68,7 @@ __device__ __forceinline__ float2 exp2_approx(float2 x) { return make_float2(exp
 __device__ __forceinline__ float2 reciprocal(float2 x) { return make_float2(reciprocal(x.x), reciprocal(x.y)); }
 
 constexpr double kLog2e = 1.4426950408889634;
-constexpr float kLeastG = -110.f, kLeastU = -250.f;
+constexpr float kLeastG = -110.f, kLeastU = -288.f;
 // x P(x^2) = tanh(x/C) up to x = C/8: y (1 - y^2/3 + 2y^4/15 - ..), what
 // follows is below 3.5 units of 2^-24
 template <int C> __device__ __forceinline__ float2 tanh_series(float2 x, double scale) {
@@ -139,8 +139,8 @@ __device__ void exp_two(float xh, float xl, Two &E, Two &less, Two &more) {
     less = plus_low(two(1.f, -E.h), -E.l);
     if (n == 0.f) less = {-m.h, -m.l};
 }
-// a(g) and b(u) (for g <= 100 and kLeastU <= u <= 700, where they have their
-// limits to 2^-48); a is taken for 0 where E^2 leaves fp32
+// a(g) and b(u) (for g <= 100 and |u| <= 700, where they have their limits to
+// 2^-48); a is taken for 0 where E^2 leaves fp32
 __device__ __forceinline__ Two situ_a(float g) {
     if (g < -87.f) return {-0.f, 0.f};
     Two E, n, d;
@@ -158,7 +158,7 @@ __device__ __forceinline__ Two situ_b(float u) {
 // h of g and u that are not NaN, rounded to the odd one of its two fp32
 // neighbours, so that rounding it on to a code rounds h itself
 __device__ __noinline__ float situ_odd(float g, float u) {
-    const Two h = times(situ_a(fminf(g, 100.f)), situ_b(fminf(fmaxf(u, kLeastU), 700.f)));
+    const Two h = times(situ_a(fminf(g, 100.f)), situ_b(fminf(fmaxf(u, -700.f), 700.f)));
     const uint32_t bits = __float_as_uint(h.h);
     if (h.l == 0.f || (bits & 1u)) return h.h;
     return __uint_as_float((h.l < 0.f) == (h.h < 0.f) ? bits + 1 : bits - 1);

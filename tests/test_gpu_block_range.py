@@ -66,3 +66,44 @@ def test_situ_of_every_extreme_with_every_other(cuda_dev, kind, many):
     exact = bright.repeat(32, 1) & ~(g < -16)
     assert np.array_equal(got[exact], want[exact])
     assert k3mx.k3mx_device_status() == (0, 0)
+
+
+def gates_at_a_middle():
+    """fp32 gates with |25 a(g)| beyond the middle of two codes by less than 1 - tanh(10) of it, and by more
+    than h is formed to."""
+    def a(g):
+        return 4 * np.tanh(g / 4) / (1 + np.exp(-g))
+    found = []
+    for lo, hi in ((2.0 ** -24, 40.0), (-1.8, -2.0 ** -24), (-16.0, -3.2)):
+        steps = np.sort(np.float32(np.sign(lo) * np.exp(np.linspace(np.log(min(abs(lo), abs(hi))), np.log(max(abs(lo), abs(hi))), 8000))))
+        v = np.abs(25 * a(steps.astype(np.float64)))
+        for i in range(len(steps) - 1):
+            e = np.floor(np.log2(min(v[i], v[i + 1])))
+            for m in (np.arange(8, 16) + 0.5) * 2.0 ** (e - 3):
+                if not min(v[i], v[i + 1]) < m < max(v[i], v[i + 1]):
+                    continue
+                l, h = np.float32(steps[i]), np.float32(steps[i + 1])          # |25 a| - m changes its sign between the two
+                up = v[i + 1] > v[i]
+                for _ in range(60):
+                    c = np.float32((np.float64(l) + np.float64(h)) / 2)
+                    if c == l or c == h:
+                        break
+                    if (abs(25 * a(np.float64(c))) > m) == up:
+                        h = c
+                    else:
+                        l = c
+                g = h if up else l                                             # the one beyond m
+                over = abs(25 * a(np.float64(g))) / m - 1
+                if 2.0 ** -28.8 < over < 2.0 ** -27.95:
+                    found.append(g)
+    return np.array(found, np.float64)
+
+
+@pytest.mark.parametrize("u", [-INF, -1000.0, -600.0, 600.0, INF])
+def test_situ_where_the_other_factor_is_next_to_its_limit(cuda_dev, u):
+    g = gates_at_a_middle()
+    assert g.size >= 3
+    x = np.concatenate([np.repeat(g[:, None], 32, 1), np.full((g.size, 32), u)], 1)
+    codes, scales, _, _ = situ(rows_of(x, "float32", 0), False)
+    want, s = mx_ref.quantize(situ_of(x[:, :32], x[:, 32:]), mx_ref.MXFP8)
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), want)
