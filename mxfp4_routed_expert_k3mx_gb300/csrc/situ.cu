@@ -556,7 +556,8 @@ __device__ __forceinline__ float half_sums(float a, float b) {
 }
 
 template <bool WARP, int V, bool BF16, int D, bool KEEP>
-__global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_grad(const NormGradArgs a) {
+__global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024, 1)
+k_norm_grad(const NormGradArgs a) {
     extern __shared__ __align__(16) uint8_t ring[];       // D > 0: [D][V] of dn, dres, codes of the CTA's threads; !KEEP: the sums
     __shared__ float sums[2][2][32];
     constexpr int kQ = BF16 ? 1 : 2, kElem = BF16 ? 2 : 4;        // kQ: 16 bytes of a run's dn
@@ -662,6 +663,16 @@ __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_g
 #pragma unroll
             for (int p = 0; p < V; p++) values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);
         }
+        auto scaled_again = [&](float by, float bd) {                 // s by, dn bd
+            if (KEEP) {
+#pragma unroll
+                for (int p = 0; p < V; p++) {
+                    values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) x[KEEP ? p : 0][j] *= by, dn[KEEP ? p : 0][j] *= bd;
+                }
+            }
+        };
         // a run's s, dn and weight: kept in registers, or fetched again
         auto run = [&](int p, float (&rx)[8], float (&rd)[8], float (&rw)[8]) {
             if (KEEP) {
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_g
         float early[8] = {};
         if (kEarly && res) grads(0, 1, early);
         float ss, sx;
-        auto sum = [&](float by) {
+        auto sum = [&](float by, float bd) {                 // the sums of s^2 and a s (KEEP: of what the registers hold)
             float2 s2 = both(0.f), x2 = both(0.f);
 #pragma unroll
             for (int p = 0; p < V; p++) {
@@ -683,9 +694,10 @@ __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_g
                 run(p, rx, rd, rw);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    const float2 v = by == 1.f ? pair(rx, j) : __fmul2_rn(pair(rx, j), both(by));
+                    const float2 v = KEEP ? pair(rx, j) : __fmul2_rn(pair(rx, j), both(by));
+                    const float2 g = KEEP ? pair(rd, j) : __fmul2_rn(pair(rd, j), both(bd));
                     s2 = __ffma2_rn(v, v, s2);
-                    x2 = __ffma2_rn(__fmul2_rn(pair(rw, j), pair(rd, j)), v, x2);
+                    x2 = __ffma2_rn(__fmul2_rn(pair(rw, j), g), v, x2);
                 }
             }
             float v = half_sums(s2.x + s2.y, x2.x + x2.y);
@@ -701,16 +713,23 @@ __global__ void __launch_bounds__(WARP ? kThreads : D > 0 ? 512 : 1024) k_norm_g
             }
             ss = __shfl_sync(0xffffffffu, v, 0), sx = __shfl_sync(0xffffffffu, v, 16);
         };
-        sum(1.f);
-        float by = 1.f, eps = a.eps;
-        if (!(ss + eps < INFINITY && fabsf(sx) < INFINITY)) {   // the same for every thread of the row
-            // sums of large values leave fp32: again of 2^-72 times the values
-            by = 0x1p-72f, eps *= 0x1p-144f;
-            sum(by);
+        sum(1.f, 1.f);
+        float m = fmaf(ss, inverse, a.eps), by = 1.f, undo = 1.f;
+        // (the same for every thread of the row)
+        if (!(m < INFINITY && fabsf(sx) < INFINITY)) {
+            // A sum leaves fp32: both again, each with what is too large of it by 2^-72.  The squares add up to 2^127 at
+            // most then; and the products to sqrt(width) |a| times the root of the squares' sum, below 2^128.
+            by = m < INFINITY ? 1.f : 0x1p-72f;
+            const float bd = fabsf(sx) < INFINITY ? 1.f : 0x1p-72f;
+            undo = fabsf(sx) < INFINITY ? 1.f : 0x1p72f;
+            scaled_again(by, bd);
+            sum(by, bd);
+            m = fmaf(ss, inverse, a.eps * by * by);
+            scaled_again(1.f, 1.f);
         }
         // k by: the factor of the values themselves, kq: dx = k a - n kq
-        const float m = fmaf(ss, inverse, eps), k0 = rsqrtf(m), k = m == 0.f ? k0 : k0 * fmaf(-0.5f, fmaf(m * k0, k0, -1.f), 1.f);
-        const float kx = k * by, kq = kx * (k * (sx * inverse));
+        const float k0 = rsqrtf(m), k = m == 0.f ? k0 : k0 * fmaf(-0.5f, fmaf(m * k0, k0, -1.f), 1.f);
+        const float kx = k * by, kq = kx * (k * (sx * inverse) * undo);
 #pragma unroll
         for (int p = 0; p < V; p++) {
             float rx[8], rd[8], rw[8], r[8] = {};

@@ -107,3 +107,84 @@ def test_situ_where_the_other_factor_is_next_to_its_limit(cuda_dev, u):
     codes, scales, _, _ = situ(rows_of(x, "float32", 0), False)
     want, s = mx_ref.quantize(situ_of(x[:, :32], x[:, 32:]), mx_ref.MXFP8)
     assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), want)
+
+
+# ---------------------------------------------------------------- the norm --
+
+def norm_backward(x, dn, weight, eps, kind):
+    """(dx, dweight) at the rows of doubles x [T, W] quantised here, and the definition's results."""
+    T, W = x.shape
+    code, s = mx_ref.quantize(x.astype(np.float32).astype(np.float64), mx_ref.MXFP8)
+    dn, g = rows_of(dn, kind, 0).contiguous(), torch.from_numpy(weight).to(DEV).bfloat16()
+    with np.errstate(all="ignore"):
+        want = block_ref.norm_backward(mx_ref.values(code, s, mx_ref.MXFP8), doubles(dn), doubles(g), np.float64(np.float32(eps)), None)
+    dx, dweight = torch.full((T, W), NAN, dtype=TYPES[kind], device=DEV), torch.full((W,), NAN, device=DEV)
+    ws = torch.full((k3mx.k3mx_rmsnorm_mx_backward_workspace_size(T, W),), 0xFF, dtype=torch.uint8, device=DEV)
+    k3mx.k3mx_rmsnorm_mx_backward(dx, dweight, dn, torch.from_numpy(code).to(DEV), torch.from_numpy(s).to(DEV), g, eps, ws)
+    return dx, dweight, want
+
+
+def check_norm(dx, dweight, want, kind, T, W):
+    """What is off, beside fp32's own range: each sum's terms in turn and 30 roundings more."""
+    wx, wg, mx, mg = want
+    tol = (W / 1024 + 32 + 30) * 2.0 ** -24 * mx
+    tol += block_ref.HALF[kind] * (np.abs(wx) + tol) + 2.0 ** -117
+    # rows whose terms fp32 holds
+    held = np.nan_to_num(mx, nan=np.inf).max(1) < 2.0 ** 127
+    got = doubles(dx)
+    assert np.all(np.abs(got - wx)[held] <= tol[held])
+    if np.isfinite(mg).all() and mg.max() < 2.0 ** 127:
+        rows = min(T / 600 + 8, 1024) + max(76, T / 8192) + 16
+        assert np.all(np.abs(doubles(dweight) - wg) <= (rows + W / 1024 + 40) * 2.0 ** -24 * mg + 2.0 ** -117)
+    return held
+
+
+def rows_of_sizes(T, W, kind, sizes, size, eps):
+    """Rows of each size and gradients of one, whose products add up or cancel."""
+    r = np.random.default_rng(5)
+    scale = np.resize(np.array(sizes), T)[:, None]
+    unit = r.normal(size=(T, W))
+    dn = np.abs(r.normal(size=(T, W))) * size
+    along = (np.arange(T) // len(sizes) % 2 == 0)[:, None]
+    dn = np.where(along, dn * np.sign(unit), dn * r.choice([-1.0, 1.0], size=(T, W)))
+    held = check_norm(*norm_backward(unit * scale, dn, 1 + 0.1 * r.normal(size=W), eps, kind), kind, T, W)
+    assert held[scale[:, 0] >= 1.0].all() and k3mx.k3mx_device_status() == (0, 0)
+
+
+NORM_SHAPES = [(24, 96), (24, 2048), (168, 2048), (24, 7168), (24, 8224), (24, 16416)]
+
+
+@pytest.mark.parametrize("T,W", NORM_SHAPES)
+@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("size", [1.0, 1e20, 3e35, 1e36])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_norm_backward_of_large_gradients(cuda_dev, T, W, kind, size, eps):
+    """Sums of squares and of products that leave fp32, each by itself and both."""
+    rows_of_sizes(T, W, kind, [1e-3, 0.125, 1.0, 1e4, 1e15, 1e19, 1e30], size, eps)
+
+
+@pytest.mark.parametrize("T,W", [(3, 96), (3, 2048), (200, 2048), (3, 8224)])
+@pytest.mark.parametrize("x,d,eps", [(1.0, 1e36, 0.0), (1e18, 1e36, 1.0)])
+def test_norm_backward_where_large_products_cancel(cuda_dev, T, W, x, d, eps):
+    alternating(T, W, x, d, eps)
+
+
+def alternating(T, W, x, d, eps):
+    """Rows of one value with gradients of alternating signs: a sum of 0 of large or small terms."""
+    s = np.full((T, W), x)
+    dn = np.full((T, W), d) * np.where(np.arange(W) % 2, 1.0, -1.0)
+    dn[1] = 0.0
+    dn[2, 5] *= 3
+    assert check_norm(*norm_backward(s, dn, np.ones(W), eps, "float32"), "float32", T, W).all()
+
+
+@pytest.mark.parametrize("W", [96, 7168])
+def test_norm_backward_of_one_value_far_above_its_row(cuda_dev, W):
+    r = np.random.default_rng(6)
+    x, dn = r.normal(size=(4, W)), np.abs(r.normal(size=(4, W))) * 1e35
+    x[0, 3], dn[0, 3] = 1e21, 0.0
+    x[1, 64], dn[1, 64] = 1e30, 0.0
+    x[2, 40] = -1e25
+    dn *= np.sign(x)
+    for kind in sorted(TYPES):
+        assert check_norm(*norm_backward(x, dn, np.ones(W), 1e-5, kind), kind, 4, W).all()
