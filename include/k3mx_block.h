@@ -152,8 +152,12 @@ k3mx_status k3mx_situ_mx_backward(void *dgu, const void *dh, int64_t lddh, int d
  *        >= k3mx_rmsnorm_mx_backward_workspace_size(...) bytes
  *   sizes as for k3mx_rmsnorm_mx.  Pointers 16-byte aligned (saved_scales:
  *   any), lddn a multiple of 16 bytes.
- * Rows are added in fp32, at most 1024 by one thread, then the parts.  A row
- * of zeros with eps = 0 has no gradient: NaN.
+ * Rows are added in fp32, at most 1024 by one thread, then the parts.  Sums of
+ * a row that leave fp32, or its normal numbers, are formed of scaled values:
+ * where sqrt(mean(s^2) + eps) >= 2^-126 and g dn, normal or 0, and what dx adds
+ * up are finite, dx is within (width / 1024 + 62) 2^-24 of the magnitudes it
+ * adds up, and within 2^-117, before its rounding.  A row of zeros with eps = 0
+ * has no gradient: NaN.
  */
 size_t k3mx_rmsnorm_mx_backward_workspace_size(int n_tokens, int width);
 k3mx_status k3mx_rmsnorm_mx_backward(void *dx, float *dweight, const void *dn, int64_t lddn, const void *dres,

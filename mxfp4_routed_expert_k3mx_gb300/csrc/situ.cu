@@ -716,14 +716,21 @@ k_norm_grad(const NormGradArgs a) {
         sum(1.f, 1.f);
         float m = fmaf(ss, inverse, a.eps), by = 1.f, undo = 1.f;
         // (the same for every thread of the row)
-        if (!(m < INFINITY && fabsf(sx) < INFINITY)) {
-            // A sum leaves fp32: both again, each with what is too large of it by 2^-72.  The squares add up to 2^127 at
-            // most then; and the products to sqrt(width) |a| times the root of the squares' sum, below 2^128.
-            by = m < INFINITY ? 1.f : 0x1p-72f;
-            const float bd = fabsf(sx) < INFINITY ? 1.f : 0x1p-72f;
-            undo = fabsf(sx) < INFINITY ? 1.f : 0x1p72f;
-            scaled_again(by, bd);
-            sum(by, bd);
+        if (!(m >= 0x1p-100f && m < INFINITY && fabsf(sx) < INFINITY && (fabsf(sx) >= 0x1p-90f || m >= 0x1p-24f))) {
+            // A sum leaves fp32, or its normal numbers: both again, of s and dn by a power of two each.  Squares above
+            // it: s by 2^-72, whose squares add up to 2^127 at most.  A mean below 2^-100, of which subnormal squares
+            // (each off by 2^-150) may be much: s by 2^64.  Products above it: dn by 2^-72 (they add up to sqrt(width)
+            // |a| times the root of the squares' sum, below 2^128 then).  Products that may be subnormal, where k^2 |n|
+            // times 2^-150 may be much, or that add up to 0: dn by 2^100, or as it is where that is too large.
+            by = !(m < INFINITY) ? 0x1p-72f : m < 0x1p-100f ? 0x1p64f : 1.f;
+            float bd = !(fabsf(sx) < INFINITY) ? 0x1p-72f : fabsf(sx) < 0x1p-90f && m < 0x1p-24f ? 0x1p100f : 1.f;
+            undo = bd < 1.f ? 0x1p72f : bd > 1.f ? 0x1p-100f : 1.f;
+            for (;;) {
+                scaled_again(by, bd);
+                sum(by, bd);
+                if (bd <= 1.f || fabsf(sx) < INFINITY) break;
+                bd = undo = 1.f;
+            }
             m = fmaf(ss, inverse, a.eps * by * by);
             scaled_again(1.f, 1.f);
         }

@@ -188,3 +188,19 @@ def test_norm_backward_of_one_value_far_above_its_row(cuda_dev, W):
     dn *= np.sign(x)
     for kind in sorted(TYPES):
         assert check_norm(*norm_backward(x, dn, np.ones(W), 1e-5, kind), kind, 4, W).all()
+
+
+@pytest.mark.parametrize("T,W", NORM_SHAPES)
+@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("size", [1e-30, 1e-10, 1.0, 1e20, 3e35])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_norm_backward_of_small_rows(cuda_dev, T, W, kind, size, eps):
+    """Sums of squares and of products that are below fp32's normal numbers, each by itself and both."""
+    rows_of_sizes(T, W, kind, [1e-36, 1e-30, 1e-23, 1e-18, 1e-13, 1e-10, 1e-5, 1.0, 1e30], size, eps)
+
+
+@pytest.mark.parametrize("T,W", [(3, 96), (3, 2048), (200, 2048), (3, 8224)])
+@pytest.mark.parametrize("x,d,eps", [(1e-15, 1e20, 0.0), (1e-15, 1e20, 1e-30), (1e-20, 0.0, 0.0), (1e-36, 0.0, 0.0), (1e-25, 1e10, 0.0),
+                                     (1e-15, 1e-30, 0.0), (1e-30, 1e-37, 0.0)])
+def test_norm_backward_where_products_of_small_rows_cancel(cuda_dev, T, W, x, d, eps):
+    alternating(T, W, x, d, eps)
