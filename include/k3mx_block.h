@@ -72,7 +72,8 @@ k3mx_status k3mx_dispatch(void *rows, uint8_t *scales, const void *x, const uint
 
 /*
  * y[t] = base[t] + sum_k w[t][k] rows[place[t][k]], in fp32, k rising, base
- * last, one rounding to y's type.
+ * last, one rounding to y's type: a token's bits do not depend on the others of
+ * the call.
  *   rows  [n_rows][width], rows_dtype K3MX_F32 or K3MX_BF16
  *   place [n_tokens][topk] as for k3mx_dispatch; skipped pairs add nothing
  *   w     [n_tokens][topk] fp32, or NULL: all 1

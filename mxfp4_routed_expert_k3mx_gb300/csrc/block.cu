@@ -7,7 +7,7 @@
 // calls, inputs larger than L2; a copy reaches 6.78 TB/s):
 //   dispatch 4096 tokens x 16, 3584 MXFP8      37.1 us, 6.3 TB/s; 1 token 1.6 us
 //   combine 65536 rows of 3584 fp32            129 us, 7.0 TB/s; bf16 76 us, 6.6
-//   combine 1 token, 16 rows of 7168 bf16      1.7 us
+//   combine 1 token, 16 rows of 7168 bf16      1.5 us
 //   its gradient, 65536 rows of 3584 bf16      155 us, 6.3 TB/s; 1 token 2.2 us
 // Rows that do not begin at multiples of 16 bytes (an odd width) are put together
 // from whole vectors by dispatch and, of bf16, by combine (32768 rows of 3001 in 83
@@ -392,10 +392,18 @@ k_dispatch_odd(T *rows, uint8_t *scales, const T *x, const uint8_t *x_scales, in
     }
 }
 
-// V consecutive values; V 8: whole vectors
+// V consecutive values; V 8: whole vectors, 2: whole pairs
 template <bool BF16, int V> __device__ __forceinline__ void load_run(const void *base, int64_t i, float (&v)[V]) {
     if constexpr (V == 8) {
         load8<BF16, true>(base, i, v);
+    } else if constexpr (V == 2) {
+        if (BF16) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + i);
+            v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xFFFF0000u);
+        } else {
+            const float2 w = *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + i);
+            v[0] = w.x, v[1] = w.y;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < V; j++)
@@ -413,6 +421,9 @@ template <bool BF16, int V> __device__ __forceinline__ void store_run(void *base
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
+    } else if constexpr (V == 2) {
+        if (BF16) *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + i) = bf16x2(v[0], v[1]);
+        else *reinterpret_cast<float2 *>(static_cast<float *>(base) + i) = make_float2(v[0], v[1]);
     } else {
 #pragma unroll
         for (int j = 0; j < V; j++) {
@@ -501,53 +512,55 @@ __global__ void __launch_bounds__(kThreads, 4) k_combine(const CombineArgs a, in
         }
 }
 
-// Few tokens: a CTA has 32 runs of one token, its eight warps a share of the
-// choices each; the shares are added in their order.  (1 token, 16 rows of 7168
-// bf16: 1.7 us on the device, 3.7 by k_combine; 8 x 3584 fp32 1.9 and 3.9; 64 x
-// 7168, 8 rows each, 4.4 and 3.8.)
+// Few tokens: a CTA has 256 / K runs of one token and brings them of K choices at
+// a time to shared memory, a run a thread; the first 1024 / K threads then add
+// two columns each, k rising as in k_combine, so that a token's bits do not depend
+// on how many others the call has.  (Device time, here and by k_combine: 1 token,
+// 16 rows of 7168 bf16 1.5 and 4.4 us, 8 x 3584 1.8 and 3.1, 36 x 7168 3.8 and
+// 5.0, 500 x 512, 8 rows each, 2.5 and 3.5; 64 x 7168, 8 rows each, 3.75 and 3.6.)
 constexpr int64_t kCombineFew = 1 << 15;      // runs of all tokens
-template <bool RB, bool YB>
+// Eight choices at a time, not sixteen: few CTAs wait for the second eight, many
+// are half as many then (1 token, 16 rows: 1.95 and 1.54 us, 8 2.15 and 1.84; 16 x
+// 7168 2.26 and 2.46, 36 3.81 and 4.00).
+constexpr int64_t kCombineEights = 1 << 13;   // runs of all tokens above which
+template <bool RB, bool YB, int K>
 __global__ void __launch_bounds__(kThreads) k_combine_few(const CombineArgs a, int chunks) {
-    __shared__ float part[kThreads / 32][256];
+    constexpr int kRuns = kThreads / K;
+    __shared__ Raw<RB> part[K][kRuns];
+    __shared__ __align__(16) float weight[K];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int u = threadIdx.x % kRuns, i = threadIdx.x / kRuns;
     const int64_t t = blockIdx.x / chunks;
-    const int c0 = (int)(blockIdx.x - t * chunks) * 256, c = c0 + 8 * lane, mine = c0 + threadIdx.x;
-    const int share = (a.topk + kThreads / 32 - 1) / (kThreads / 32), k1 = min((warp + 1) * share, a.topk);
-    float base[1] = {0.f}, acc[8] = {};
-    if (a.base != nullptr && mine < a.width) load_run<YB, 1>(a.base, t * a.width + mine, base);
-    for (int k0 = warp * share; k0 < k1; k0 += 2) {
-        int r[2];
-        float w[2];
-        Raw<RB> v[2];
+    const int c0 = (int)(blockIdx.x - t * chunks) * 8 * kRuns, c = c0 + 8 * u, mine = c0 + 2 * threadIdx.x;
+    const bool adds = threadIdx.x < 4 * kRuns && mine < a.width;
+    float base[2] = {0.f, 0.f}, acc[2] = {0.f, 0.f};
+    if (a.base != nullptr && adds) load_run<YB, 2>(a.base, t * a.width + mine, base);
+    for (int k0 = 0; k0 < a.topk; k0 += K) {
+        const int k = k0 + i;
+        const int64_t p = t * a.topk + k;
+        const int r = k < a.topk ? row_of(a.place[p], a.n_rows, c == 0, (int)p, a.status) : -1;
+        const float w = r < 0 ? 0.f : a.w != nullptr ? a.w[p] : 1.f;
+        Raw<RB> v;
+        v.minus_zero();                            // (0 times -0 leaves any sum as it is)
+        if (r >= 0 && c < a.width) v.load(a.rows, (int64_t)r * a.width + c);
+        if (k0 > 0) __syncthreads();
+        if (u == 0) weight[i] = w;
+        part[i][u] = v;
+        __syncthreads();
+        if (adds) {
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int64_t p = t * a.topk + k0 + j;
-            r[j] = k0 + j < k1 ? row_of(a.place[p], a.n_rows, c == 0, (int)p, a.status) : -1;
-            w[j] = r[j] >= 0 && a.w != nullptr ? a.w[p] : 1.f;
-            v[j].zero();
-            if (r[j] >= 0 && c < a.width) v[j].load(a.rows, (int64_t)r[j] * a.width + c);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; j++)
-            if (r[j] >= 0) {
-                float x[8];
-                v[j].values(x);
-#pragma unroll
-                for (int q = 0; q < 8; q++) acc[q] = fmaf(w[j], x[q], acc[q]);
+            for (int j = 0; j < K; j++) {
+                float x[2];
+                load_run<RB, 2>(part[j], 2 * threadIdx.x, x);
+                acc[0] = fmaf(weight[j], x[0], acc[0]);
+                acc[1] = fmaf(weight[j], x[1], acc[1]);
             }
+        }
     }
-    float4 *to = reinterpret_cast<float4 *>(&part[warp][8 * lane]);
-    to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    __syncthreads();
-    if (mine < a.width) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; w++) s[0] += part[w][threadIdx.x];
-        s[0] += base[0];
-        store_run<YB, 1>(a.y, t * a.width + mine, s);
+    if (adds) {
+        acc[0] += base[0], acc[1] += base[1];
+        store_run<YB, 2>(a.y, t * a.width + mine, acc);
     }
 }
 
@@ -881,9 +894,15 @@ template <bool RB, bool YB> static cudaError_t combine_t(const Ctx &c, const Com
         const int chunks = (a.width + 4 * threads - 1) / (4 * threads);
         return launch_pdl(k_combine_odd<RB, YB>, dim3((unsigned)((int64_t)a.n_tokens * chunks)), dim3(threads), 0, c.stream, a, chunks);
     }
-    const int runs = a.width / 8, chunks = (runs + 31) / 32;
-    if ((int64_t)a.n_tokens * runs <= kCombineFew && a.topk > 2)
-        return launch_pdl(k_combine_few<RB, YB>, dim3((unsigned)(a.n_tokens * chunks)), dim3(kThreads), 0, c.stream, a, chunks);
+    const int runs = a.width / 8;
+    if ((int64_t)a.n_tokens * runs <= kCombineFew && a.topk > 2) {
+        auto few = [&](auto kernel, int per) {
+            const int chunks = (runs + per - 1) / per;
+            return launch_pdl(kernel, dim3((unsigned)(a.n_tokens * chunks)), dim3(kThreads), 0, c.stream, a, chunks);
+        };
+        return a.topk <= 8 || (int64_t)a.n_tokens * runs > kCombineEights ? few(k_combine_few<RB, YB, 8>, kThreads / 8)
+                                                                          : few(k_combine_few<RB, YB, 16>, kThreads / 16);
+    }
     auto go = [&](auto kernel, int per) {
         // (CTAs of 64 threads, or of 256 that share 4 tokens and more)
         const int threads = (runs + per - 1) / per, parts = (threads + 63) / 64;

@@ -167,6 +167,10 @@ template <bool BF16> struct Raw {
         if (!BF16) q[BF16 ? 0 : 1] = p[1];
     }
     __device__ __forceinline__ void zero() { q[0] = q[BF16 ? 0 : 1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void minus_zero() {
+        constexpr uint32_t z = BF16 ? 0x80008000u : 0x80000000u;
+        q[0] = q[BF16 ? 0 : 1] = make_uint4(z, z, z, z);
+    }
     __device__ __forceinline__ void values(float (&v)[8]) const {
         const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[BF16 ? 0 : 1].x, q[BF16 ? 0 : 1].y, q[BF16 ? 0 : 1].z, q[BF16 ? 0 : 1].w};
 #pragma unroll
