@@ -535,6 +535,7 @@ NormShape norm_shape(int n_tokens, int width) {
 }
 // bytes that a thread keeps of a run: dn, dres, codes
 constexpr int run_bytes(bool bf16) { return 8 + 2 * (bf16 ? 16 : 32); }
+static_assert(3 * 512 * 2 * run_bytes(false) <= kNormSmem, "three rows of 1024 runs have to fit");
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -895,9 +896,7 @@ cudaError_t launch_norm_grad(const Ctx &c, const NormGradArgs &a, int bf16) {
                               : norm_grad_t<true, 4, 3, true>(c, a, s, bf16);
         if (s.few) return norm_grad_t<false, 1, 0, true>(c, a, s, bf16);
         if (s.threads <= 512)
-            return 4 * row <= kNormSmem   ? norm_grad_t<false, 2, 4, true>(c, a, s, bf16)
-                   : 3 * row <= kNormSmem ? norm_grad_t<false, 2, 3, true>(c, a, s, bf16)
-                                          : norm_grad_t<false, 2, 2, true>(c, a, s, bf16);
+            return 4 * row <= kNormSmem ? norm_grad_t<false, 2, 4, true>(c, a, s, bf16) : norm_grad_t<false, 2, 3, true>(c, a, s, bf16);
         return s.v == 2 ? norm_grad_t<false, 2, 0, false>(c, a, s, bf16) : norm_grad_t<false, 4, 0, false>(c, a, s, bf16);
     };
     const cudaError_t e = go();
