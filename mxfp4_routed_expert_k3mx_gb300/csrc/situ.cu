@@ -512,6 +512,10 @@ __global__ void __launch_bounds__(kTableThreads, 2) k_situ_grad_table(const Situ
 constexpr int kNormSms = 152;         // parts are a multiple of it (a constant: results do not depend on the device)
 constexpr int kRowsOfPart = 1024;     // rows that one thread adds, at most
 constexpr int kNormSmem = 220 << 10;
+// rows copied ahead (4096 x 7168: of bf16 39.2 us, three 39.9, four 40.5, one
+// 57.7; of fp32 85.2, three 85.7, one 113; 8192 x 512 bf16 10.4, three 10.6, one
+// 12.7)
+constexpr int kNormRing = 2;
 
 struct NormShape {
     bool warp;         // a row to a warp, eight a CTA
@@ -535,7 +539,7 @@ NormShape norm_shape(int n_tokens, int width) {
 }
 // bytes that a thread keeps of a run: dn, dres, codes
 constexpr int run_bytes(bool bf16) { return 8 + 2 * (bf16 ? 16 : 32); }
-static_assert(3 * 512 * 2 * run_bytes(false) <= kNormSmem, "three rows of 1024 runs have to fit");
+static_assert(kNormRing * 512 * 2 * run_bytes(false) <= kNormSmem, "the rows of 1024 runs have to fit");
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -888,15 +892,13 @@ static cudaError_t norm_grad_t(const Ctx &c, const NormGradArgs &a, const NormSh
 
 cudaError_t launch_norm_grad(const Ctx &c, const NormGradArgs &a, int bf16) {
     const NormShape s = norm_shape(a.n_tokens, a.width);
-    const int row = s.threads * s.v * run_bytes(bf16);    // shared memory of a row
     auto go = [&] {
         if (s.warp)
-            return s.v == 1   ? norm_grad_t<true, 1, 4, true>(c, a, s, bf16)
-                   : s.v == 2 ? norm_grad_t<true, 2, 3, true>(c, a, s, bf16)
-                              : norm_grad_t<true, 4, 3, true>(c, a, s, bf16);
+            return s.v == 1   ? norm_grad_t<true, 1, kNormRing, true>(c, a, s, bf16)
+                   : s.v == 2 ? norm_grad_t<true, 2, kNormRing, true>(c, a, s, bf16)
+                              : norm_grad_t<true, 4, kNormRing, true>(c, a, s, bf16);
         if (s.few) return norm_grad_t<false, 1, 0, true>(c, a, s, bf16);
-        if (s.threads <= 512)
-            return 4 * row <= kNormSmem ? norm_grad_t<false, 2, 4, true>(c, a, s, bf16) : norm_grad_t<false, 2, 3, true>(c, a, s, bf16);
+        if (s.threads <= 512) return norm_grad_t<false, 2, kNormRing, true>(c, a, s, bf16);
         return s.v == 2 ? norm_grad_t<false, 2, 0, false>(c, a, s, bf16) : norm_grad_t<false, 4, 0, false>(c, a, s, bf16);
     };
     const cudaError_t e = go();
