@@ -5,8 +5,8 @@
 // in whole vectors, with enough of them on their way, and for few tokens that
 // a call is one latency after another as seldom as can be.  Measured (repeated
 // calls, inputs larger than L2; a copy reaches 6.78 TB/s):
-//   dispatch 4096 tokens x 16, 3584 MXFP8      37.1 us, 6.3 TB/s; 1 token 1.6 us
-//   combine 65536 rows of 3584 fp32            129 us, 7.0 TB/s; bf16 76 us, 6.6
+//   dispatch 4096 tokens x 16, 3584 MXFP8      41 us, 6.3 TB/s; 1 token 1.6 us
+//   combine 65536 rows of 3584 fp32            141 us, 7.1 TB/s; bf16 75 us, 6.6
 //   combine 1 token, 16 rows of 7168 bf16      1.5 us
 //   its gradient, 65536 rows of 3584 bf16      155 us, 6.3 TB/s; 1 token 2.2 us
 // Rows that do not begin at multiples of 16 bytes (an odd width) are put together
@@ -910,6 +910,9 @@ template <bool RB, bool YB> static cudaError_t combine_t(const Ctx &c, const Com
         const int64_t tiles = (a.n_tokens + by - 1) / by;
         return launch_pdl(kernel, dim3((unsigned)(tiles * parts)), dim3(bx, by), 0, c.stream, a, runs, parts);
     };
+    // two runs a thread of bf16 rows (65536 of 3584 75 us, one 79, four 167; 2 x 8192
+    // of 7168 84, 117, 122), one of fp32 (141, two 311); two choices at a time where
+    // there are no more (2 x 8192 of 7168 bf16 84 us, four 98; 1 x 16384 147 and 176)
     constexpr int R = RB ? 2 : 1;
     return a.topk <= 2 ? go(k_combine<RB, YB, R, 2>, R) : go(k_combine<RB, YB, R, 4>, R);
 }

@@ -6,9 +6,9 @@
 //   SiTU 65536 x 2048 bf16, saved       242 us, 3.9 TB/s; not saved 177 us
 //   SiTU 32768 x 2048 fp32, saved       139 us, 5.4 TB/s
 //   its gradient, 65536 x 2048 bf16     173 us, 6.3 TB/s; 32768 fp32 150 us, 6.3
-//   norm's gradient, 4096 x 7168 bf16   40 us, 5.2 TB/s; fp32 88 us, 4.4
-//   16 x 2048: SiTU 2.3 us; 64 x 7168: norm's gradient 5.0 us (two kernels)
-// bf16 SiTU is bound by the integer pipe (81 % busy: bits to places, values to
+//   norm's gradient, 4096 x 7168 bf16   39 us, 5.3 TB/s; fp32 88 us, 4.3
+//   16 x 2048: SiTU 2.3 us; 64 x 7168: norm's gradient 4.8 us (two kernels)
+// bf16 SiTU is bound by the integer pipe (80 % busy: bits to places, values to
 // codes), the gradients by HBM, the norm's by what its 14 warps an SM leave idle
 // around a row's barrier (51 % of the issue slots used) and, in fp32, by shared
 // memory's traffic.
@@ -20,7 +20,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-constexpr int kSituCtas = 3, kSituWaves = 4;    // CTAs of k_situ an SM holds, and the rounds of them in its grid
+// CTAs of k_situ an SM holds, and the rounds of them in its grid (8.4 M runs of
+// fp32, saved: 139 us, by two CTAs 148, four 151; in one round 142, two 139,
+// sixteen 144; 0.5 M of bf16 13.7, 14.5, 15.3; 12.5, 12.4, 15.4)
+constexpr int kSituCtas = 3, kSituWaves = 4;
 
 // 8 e4m3 codes -> their values times `up`
 __device__ __forceinline__ void from_e4m3x8(uint2 q, float up, float (&v)[8]) {
@@ -97,7 +100,10 @@ __device__ __forceinline__ float2 situ2(float2 g, float2 u, double bias) {
     const float2 rc = reciprocal(__ffma2_rn(E, E, both(1.f))), rd = reciprocal(__fmul2_rn(e1, f1));
     return __fmul2_rn(__fmul2_rn(__fmul2_rn(ng, nu), rd), rc);
 }
-// The same to 2^-29 (relative, where h is above 2^-96), in sums of two floats.
+// The same to 2^-29 (relative, where h is above 2^-96), in sums of two floats:
+// Knuth's error-free sum of two numbers, products whose error a fused product
+// and sum gives exactly, and Cody and Waite's reduction of an exponential's
+// argument, by the first bits of ln 2 and the rest of it.
 struct Two {
     float h, l;
 };
@@ -121,7 +127,8 @@ __device__ __forceinline__ Two over(Two a, Two b) {
 // e^x, 1 - e^x and 1 + e^x of x = xh + xl: 2^n times the series of what is left
 __device__ void exp_two(float xh, float xl, Two &E, Two &less, Two &more) {
     constexpr double kLn2 = 0.6931471805599453;
-    constexpr float kHigh = 0.693145751953125f, kLow = (float)(kLn2 - 0.693145751953125);    // (n kHigh is exact)
+    constexpr double kBits = (int)(kLn2 * 32768) / 32768.0;                      // ln 2 to 15 bits: n kHigh is exact
+    constexpr float kHigh = (float)kBits, kLow = (float)(kLn2 - kBits);
     constexpr float kSixth = (float)(1.0 / 6);
     const float n = rintf(__fmul_rn(xh, (float)kLog2e)), p = __fmul_rn(n, kLow);
     const Two r = plus_low(two(fmaf(n, -kHigh, xh), -p), __fsub_rn(xl, fmaf(n, kLow, -p)));
@@ -265,7 +272,11 @@ __global__ void __launch_bounds__(kThreads, kSituCtas) k_situ(const SituArgs a, 
 // each rounded once, looked up by the value's bits; h is their product, within 4
 // units of 2^-24 of itself, and hardly any value has to be formed again.  Places
 // are clamped to the tables; a value that this changed (zeros, Inf and NaN among
-// them) is worked out by itself.
+// them) is worked out by itself.  The codes are h's for any g here.  By tables and
+// without, us: 16.8 M runs, saved, 242 and 258, 8.4 M 126 and 132, 4.2 M 68 and 70, 2.1 M
+// 39.7 and 38.1, 1 M 24.3 and 22.2, 0.5 M 17.5 and 13.7; not saved 177 and 194, 94 and
+// 101, 53 and 55, 31.3 and 30.6, 20.1 and 18.7, 15.0 and 11.4: from 4 M runs on they
+// are faster.
 constexpr int kLowG = (127 - 14) * 128, kCountG = 21 * 128, kLowU = (127 - 13) * 128, kCountU = 22 * 128;
 constexpr uint32_t kNearTable = 6;
 constexpr int kSituTableThreads = 1024;       // (two CTAs of 512, with a table each, take 5 % more)
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(kTableThreads, 2) k_situ_grad_table(const Situ
 // A thread has the same runs of every row, so what it needs of the next rows it
 // copies ahead into shared memory for itself (cp.async, D rows deep, no
 // barrier).  D = 0: they come from global memory, for a CTA's only row (64 rows
-// of 7168 fp32: 5.5 us, by way of shared memory 6.5) and for rows that shared
+// of 7168 fp32: 4.8 us, by way of shared memory 6.5) and for rows that shared
 // memory does not hold: those are read before the sums and from L2 once more
 // after them (KEEP false), and the sums of dn n have the shared memory.
 
@@ -522,6 +533,9 @@ struct NormShape {
     bool few;          // one row a CTA
     int v, threads, parts;
 };
+// A warp a row up to 128 runs (8192 x 1024 bf16 15.5 us, fp32 30.4; by a CTA a row
+// 18.0 and 33.5); two runs a thread of a CTA (4096 x 7168 bf16: 41 us with four
+// rows ahead, one 59), four where 1024 threads do not reach otherwise.
 NormShape norm_shape(int n_tokens, int width) {
     const int runs = width / 8;
     NormShape s;
