@@ -682,13 +682,18 @@ k_norm_grad(const NormGradArgs a) {
 #pragma unroll
             for (int p = 0; p < V; p++) values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);
         }
+        // g bd; beside an s of 0, where the product is 0, not an infinite one
+        auto up = [](float g, float bd, float s) { return bd > 1.f && s == 0.f ? 0.f : g * bd; };
         auto scaled_again = [&](float by, float bd) {                 // s by, dn bd
             if (KEEP) {
 #pragma unroll
                 for (int p = 0; p < V; p++) {
                     values(p, x[KEEP ? p : 0]), grads(p, 0, dn[KEEP ? p : 0]);
 #pragma unroll
-                    for (int j = 0; j < 8; j++) x[KEEP ? p : 0][j] *= by, dn[KEEP ? p : 0][j] *= bd;
+                    for (int j = 0; j < 8; j++) {
+                        float &s = x[KEEP ? p : 0][j], &g = dn[KEEP ? p : 0][j];
+                        s *= by, g = up(g, bd, s);
+                    }
                 }
             }
         };
@@ -714,7 +719,7 @@ k_norm_grad(const NormGradArgs a) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const float2 v = KEEP ? pair(rx, j) : __fmul2_rn(pair(rx, j), both(by));
-                    const float2 g = KEEP ? pair(rd, j) : __fmul2_rn(pair(rd, j), both(bd));
+                    const float2 g = KEEP ? pair(rd, j) : make_float2(up(rd[j], bd, v.x), up(rd[j + 1], bd, v.y));
                     s2 = __ffma2_rn(v, v, s2);
                     x2 = __ffma2_rn(__fmul2_rn(pair(rw, j), g), v, x2);
                 }

@@ -204,3 +204,13 @@ def test_norm_backward_of_small_rows(cuda_dev, T, W, kind, size, eps):
                                      (1e-15, 1e-30, 0.0), (1e-30, 1e-37, 0.0)])
 def test_norm_backward_where_products_of_small_rows_cancel(cuda_dev, T, W, x, d, eps):
     alternating(T, W, x, d, eps)
+
+
+@pytest.mark.parametrize("T,W", [(3, 96), (3, 2048), (200, 2048), (3, 8224), (3, 16416)])
+@pytest.mark.parametrize("kind", sorted(TYPES))
+def test_norm_backward_of_small_rows_with_large_gradients_at_zeros(cuda_dev, T, W, kind):
+    """Gradients that no scaled product may take part in, where s is 0, beside products of 1e-44."""
+    r = np.random.default_rng(9)
+    s, dn = np.abs(r.normal(size=(T, W))) * 1e-14, np.abs(r.normal(size=(T, W))) * 1e-30
+    s[:, 5::32], dn[:, 5::32] = 0.0, 1e12
+    assert check_norm(*norm_backward(s, dn, np.ones(W), 0.0, kind), kind, T, W).all() and k3mx.k3mx_device_status() == (0, 0)
